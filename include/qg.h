@@ -486,6 +486,142 @@ qg_status qg_gemm_w4a16_noalloc(const void *x, int64_t ldx, const int32_t *qweig
                                 int64_t K, qg_stream_t stream);
 
 /*
+ * Norm, 4-bit cache and attention: the rest of a decoder layer whose linear
+ * layers are the GEMMs above.  (The pages describe no such calls.)
+ *
+ * qg_rmsnorm_quantize_int8 -- residual addition, RMS norm and symmetric per-row
+ * int8 codes in one pass: the operand of qg_gemm_w8a8 and its variants.  For
+ * every row:
+ *   h = x + residual            (binary32 sum, rounded to dtype; h = x without)
+ *   p = h * weight              (exact in binary32)
+ *   a = max(max_k |p|, 1e-30)
+ *   q = clamp(rint(p * (127/a)), -127, 127)     (as qg_quantize_rowwise_int8)
+ *   x_scale = a / 127 * 1 / sqrt(mean_k h^2 + eps)
+ * so q * x_scale is the normed row: the norm's factor, common to the row, does
+ * not enter the codes, which are bit-exact IEEE operations; the sum of squares
+ * is taken in binary32.  A row with a NaN, an infinity or a value whose product
+ * or square sum leaves binary32 gets x_scale = NaN and codes 0.
+ *
+ *   x         [in]  device, [M, ldx] of dtype (QG_F16 or QG_BF16), ldx % 8 == 0
+ *   residual  [in]  device, [M, ldr], ldr % 8 == 0, or NULL
+ *   weight    [in]  device, [K] of dtype, 16-byte aligned
+ *   eps       > 0
+ *   xq        [out] device, int8 [M, ldxq], ldxq % 16 == 0
+ *   x_scale   [out] device, float32 [M]
+ *   residual_out [out] device, [M, ldro], ldro % 8 == 0: h; NULL exactly when
+ *                residual is.  It may be residual or x itself (same pointer and
+ *                leading dimension), not another overlap.
+ * K >= 1.
+ */
+qg_status qg_rmsnorm_quantize_int8(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                                   const void *weight, int dtype, float eps, int8_t *xq, int64_t ldxq,
+                                   float *x_scale, void *residual_out, int64_t ldro, int64_t M, int64_t K,
+                                   qg_stream_t stream);
+
+/*
+ * qg_dequantize_rowwise_int8 -- the values that int8 rows stand for:
+ * y[m,k] = xq[m,k] * x_scale[m] (binary32, rounded once to y_dtype).
+ *   xq [in] int8 [M, ldxq], ldxq % 16 == 0;  x_scale [in] float32 [M]
+ *   y [out] [M, ldy] of QG_F32, QG_F16 or QG_BF16, rows on 16-byte boundaries
+ */
+qg_status qg_dequantize_rowwise_int8(const int8_t *xq, int64_t ldxq, const float *x_scale, void *y, int y_dtype,
+                                     int64_t ldy, int64_t M, int64_t K, qg_stream_t stream);
+
+/*
+ * A paged key/value cache in 4 bits.  Slot s is token s % page_size of page
+ * s / page_size.  A token's head holds, for keys and for values,
+ *   codes   word [j, g] of int32 [num_pages, num_heads, page_size, 8, head_dim/64]:
+ *           channels 64 g + 8 j .. + 7, channel i of them in bits 4 i
+ *   params  fp16 [num_pages, num_heads, page_size, head_dim/64, 2]: scale and
+ *           offset of each group of 64 channels;  value = scale * code + offset
+ * Arrays are dense and 16-byte aligned.  head_dim is 64 or 128, page_size a
+ * multiple of 16 (QG_ERR_INVALID_ARG otherwise; other head_dim
+ * QG_ERR_UNSUPPORTED).
+ */
+typedef struct {
+    int32_t *k_codes;
+    void *k_params;
+    int32_t *v_codes;
+    void *v_params;
+    int64_t num_pages, num_heads, page_size, head_dim;
+} qg_kv4_cache;
+
+/*
+ * qg_quantize_kv4 -- quantize the keys and values of T tokens as they are
+ * written to the cache.  For every group of 64 channels:
+ *   lo, hi = min and max of the values x held to +-65504   (NaN propagates)
+ *   scale = fp16(max((hi - lo) / 15, 1e-5));  offset = fp16(lo)
+ *   code = clamp(rint((x - offset) / scale), 0, 15)   (binary32)
+ * A group with a NaN has scale = offset = NaN and codes 0.
+ *
+ *   k, v      [in]  device, [T, num_heads, head_dim] of dtype (QG_F16 or
+ *             QG_BF16); token and head strides in elements, multiples of 8
+ *   slots     [in]  device, int64 [T]: where each token goes.  A negative slot
+ *             skips its token (padding).  Slots of one call are distinct; with a
+ *             slot given twice, its words come from either token.  A slot
+ *             beyond the cache is skipped and qg_check_device_errors then
+ *             returns QG_ERR_INVALID_ARG.
+ *   cache     [in]  host struct; its arrays are written
+ */
+qg_status qg_quantize_kv4(const void *k, int64_t k_stride_t, int64_t k_stride_h, const void *v, int64_t v_stride_t,
+                          int64_t v_stride_h, int dtype, const int64_t *slots, const qg_kv4_cache *cache,
+                          int64_t T, qg_stream_t stream);
+
+/*
+ * qg_dequantize_kv4 -- read T tokens back: scale * code + offset (binary32,
+ * rounded once to dtype, which may be QG_F32 too).  A negative slot, and one
+ * beyond the cache (also reported by qg_check_device_errors), reads as zeros.
+ * Arguments as qg_quantize_kv4, k and v [out] with strides in multiples of 16
+ * bytes.
+ */
+qg_status qg_dequantize_kv4(const qg_kv4_cache *cache, const int64_t *slots, void *k, int64_t k_stride_t,
+                            int64_t k_stride_h, void *v, int64_t v_stride_t, int64_t v_stride_h, int dtype,
+                            int64_t T, qg_stream_t stream);
+
+/*
+ * qg_attention_kv4 -- attention of T query tokens, those of B sequences back to
+ * back, over the sequences' keys and values in the cache.
+ *   out[t, hq] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[t, hq] . k_j)
+ * with keys and values of head hq / (heads_q / num_heads).  The n query tokens
+ * of a sequence of length L (the cache already holds them) are its last ones:
+ * token i is at position L - n + i.  It sees the positions j < L with
+ *   j <= its own (causal != 0), and  j > its own - window (window > 0).
+ * A query that sees nothing gives zeros (and lse = -inf).  Scores, sums and
+ * outputs are held in binary32; the keys' and values' dequantized form, or the
+ * probabilities times the values' scale, are rounded to fp16 for the tensor cores.
+ *
+ *   q          [in]  device, [T, heads_q, head_dim] of dtype (QG_F16 or
+ *              QG_BF16); strides in elements, multiples of 8.  heads_q is a
+ *              multiple of the cache's num_heads.
+ *   block_table [in] device, int32 [B, ld_table]: the pages of each sequence in
+ *              order; entries that cover its length are read
+ *   seq_lens   [in]  device, int32 [B]: L
+ *   q_starts   [in]  device, int32 [B + 1]: sequence b's query tokens are rows
+ *              q_starts[b] .. q_starts[b+1] - 1, or NULL: T / B tokens each
+ *   scale      > 0
+ *   out        [out] device, [T, heads_q, head_dim] of dtype, strides as q.
+ *              Rows behind q_starts[B] are not written.
+ *   lse        [out] device, float32 [T, heads_q], or NULL: log sum_j p_j
+ *   workspace  device scratch of qg_attention_kv4_workspace_size() bytes (0: may
+ *              be NULL), 16-byte aligned, contents free before and after.  Calls
+ *              that may run at the same time must not share it.
+ * B is at most 4096.  A length or start outside its range is cut, a page index
+ * outside the cache is not read; the sequence's result is then undefined and
+ * qg_check_device_errors returns QG_ERR_INVALID_ARG.
+ */
+qg_status qg_attention_kv4(const void *q, int64_t q_stride_t, int64_t q_stride_h, const qg_kv4_cache *cache,
+                           const int32_t *block_table, int64_t ld_table, const int32_t *seq_lens,
+                           const int32_t *q_starts, float scale, int causal, int64_t window, void *out,
+                           int64_t out_stride_t, int64_t out_stride_h, int dtype, float *lse, int64_t B, int64_t T,
+                           int64_t heads_q, int64_t max_pages, void *workspace, size_t workspace_bytes,
+                           qg_stream_t stream);
+
+/* Bytes of workspace for qg_attention_kv4 on the current device (ragged != 0:
+ * with q_starts). */
+size_t qg_attention_kv4_workspace_size(int64_t B, int64_t T, int64_t heads_q, int64_t num_heads, int64_t head_dim,
+                                       int ragged);
+
+/*
  * Launch plans.  The pages describe no such call: it exists for loops that
  * issue the same call with the same preallocated buffers again and again (a
  * decode step per token), where the caller's per-call argument marshalling
@@ -496,7 +632,10 @@ qg_status qg_gemm_w4a16_noalloc(const void *x, int64_t ldx, const int32_t *qweig
  * qg_gemm_w8a8_ex, qg_gemm_w8a16_ex and qg_gemm_w4a16_ex (everything but the
  * stream; same meaning, layouts and flags) into a new plan stored in *plan;
  * qg_plan_launch(plan, stream) then makes that call on `stream` and returns
- * its status.
+ * its status.  qg_plan_rmsnorm_quantize_int8, qg_plan_quantize_kv4 and
+ * qg_plan_attention_kv4 do the same for qg_rmsnorm_quantize_int8,
+ * qg_quantize_kv4 and qg_attention_kv4 (the cache struct is copied; launches of
+ * one attention plan share its workspace, so they must not overlap).
  *   - A plan holds the pointers and sizes, not the data: the caller keeps
  *     every buffer alive while the plan is launched and may rewrite the
  *     buffers' contents between launches (new activations, in place).
@@ -524,6 +663,19 @@ qg_status qg_plan_gemm_w4a16(qg_plan **plan, const void *x, int64_t ldx, const i
                              const void *scale, const void *zero, int64_t group, const float *bias, void *y,
                              int64_t ldy, int64_t M, int64_t N, int64_t K, void *workspace,
                              size_t workspace_bytes, unsigned flags);
+qg_status qg_plan_rmsnorm_quantize_int8(qg_plan **plan, const void *x, int64_t ldx, const void *residual,
+                                        int64_t ldr, const void *weight, int dtype, float eps, int8_t *xq,
+                                        int64_t ldxq, float *x_scale, void *residual_out, int64_t ldro, int64_t M,
+                                        int64_t K);
+qg_status qg_plan_quantize_kv4(qg_plan **plan, const void *k, int64_t k_stride_t, int64_t k_stride_h, const void *v,
+                               int64_t v_stride_t, int64_t v_stride_h, int dtype, const int64_t *slots,
+                               const qg_kv4_cache *cache, int64_t T);
+qg_status qg_plan_attention_kv4(qg_plan **plan, const void *q, int64_t q_stride_t, int64_t q_stride_h,
+                                const qg_kv4_cache *cache, const int32_t *block_table, int64_t ld_table,
+                                const int32_t *seq_lens, const int32_t *q_starts, float scale, int causal,
+                                int64_t window, void *out, int64_t out_stride_t, int64_t out_stride_h, int dtype,
+                                float *lse, int64_t B, int64_t T, int64_t heads_q, int64_t max_pages,
+                                void *workspace, size_t workspace_bytes);
 qg_status qg_plan_launch(const qg_plan *plan, qg_stream_t stream);
 void qg_plan_destroy(qg_plan *plan);
 

@@ -11,8 +11,14 @@ Functions (same names as the C entry points, minus the ``qg_`` prefix):
     gemm_w8a8(xq, wq, x_scale, w_scale, bias=None, out_dtype=torch.float16) -> y [M,N]
     gemm_w8a16(x, wq, w_scale, bias=None)       -> y fp16 [M,N]
     gemm_w4a16(x, qweight, scale, zero, group=64, bias=None) -> y fp16 [M,N]
+    rmsnorm_quantize_int8(x, weight, residual=None) -> (xq int8 [M,K], x_scale f32 [M], h or None)
+    dequantize_rowwise_int8(xq, x_scale)        -> y [M,K]
+    kv4_cache(num_pages, num_heads, head_dim)   -> KV4Cache (a paged 4-bit key/value cache)
+    quantize_kv4(k, v, cache, slots) / dequantize_kv4(cache, slots) -> (k, v)
+    attention_kv4(q, cache, block_table, seq_lens) -> out [T,Hq,D]
 Launch plans bind one call's arguments once for loops over preallocated buffers:
     plan_quantize_rowwise_int8 / plan_gemm_w8a8 / plan_gemm_w8a16 / plan_gemm_w4a16
+    plan_rmsnorm_quantize_int8 / plan_quantize_kv4 / plan_attention_kv4
     (same arguments as the calls)           -> Plan; plan.launch(stream=None), plan.out
 The GEMMs take workspace=None (the default: decode shapes run the cluster
 split-K kernels, no scratch memory), "auto" (a per-stream workspace kept by this
@@ -23,8 +29,10 @@ column-major [K, N] weight).  ``raw`` exposes the ctypes library itself.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -42,6 +50,7 @@ _DTYPE_CODE = {torch.float32: QG_F32, torch.float16: QG_F16, torch.bfloat16: QG_
 
 # C signatures of every exported symbol of include/qg.h.
 _i64, _vp, _int, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_f32 = ctypes.c_float
 _pp = ctypes.POINTER(ctypes.c_void_p)
 SIGNATURES = {
     "qg_status_string": ([_int], ctypes.c_char_p),
@@ -82,6 +91,19 @@ SIGNATURES = {
                             ctypes.c_uint], _int),
     "qg_plan_gemm_w4a16": ([_pp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _sz,
                             ctypes.c_uint], _int),
+    "qg_rmsnorm_quantize_int8": ([_vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp, _vp, _i64, _i64, _i64,
+                                  _vp], _int),
+    "qg_dequantize_rowwise_int8": ([_vp, _i64, _vp, _vp, _int, _i64, _i64, _i64, _vp], _int),
+    "qg_quantize_kv4": ([_vp, _i64, _i64, _vp, _i64, _i64, _int, _vp, _vp, _i64, _vp], _int),
+    "qg_dequantize_kv4": ([_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, _i64, _vp], _int),
+    "qg_attention_kv4": ([_vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _f32, _int, _i64, _vp, _i64, _i64, _int, _vp,
+                          _i64, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    "qg_attention_kv4_workspace_size": ([_i64, _i64, _i64, _i64, _i64, _int], _sz),
+    "qg_plan_rmsnorm_quantize_int8": ([_pp, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp, _vp, _i64, _i64,
+                                       _i64], _int),
+    "qg_plan_quantize_kv4": ([_pp, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp, _vp, _i64], _int),
+    "qg_plan_attention_kv4": ([_pp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _f32, _int, _i64, _vp, _i64, _i64,
+                               _int, _vp, _i64, _i64, _i64, _i64, _vp, _sz], _int),
     "qg_plan_launch": ([_vp, _vp], _int),
     "qg_plan_destroy": ([_vp], None),
 }
@@ -548,6 +570,264 @@ def gemm_w4a16_noalloc(x: torch.Tensor, qweight: torch.Tensor, scale: torch.Tens
 
 
 # ---------------------------------------------------------------------------
+# Norm, 4-bit cache and attention
+# ---------------------------------------------------------------------------
+_HALF = (torch.float16, torch.bfloat16)
+
+
+def _one_device(**tensors) -> torch.device:
+    """The CUDA device that all given tensors (None: absent) lie on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+    return dev
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(dev: torch.device):
+    """A context in which `dev` is the current device (and _stream() its stream)."""
+    return _SAME_DEVICE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _half_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _HALF:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    return _DTYPE_CODE[t.dtype]
+
+
+def _shape2(t: torch.Tensor, name: str, M: int, K: int) -> None:
+    if tuple(t.shape) != (M, K):
+        raise ValueError(f"{name} must be [{M}, {K}], got {tuple(t.shape)}")
+
+
+def _rmsnorm_args(x, weight, residual, eps, out, scale_out, residual_out):
+    """((xq, x_scale, h or None), device, the C arguments but the stream) of qg_rmsnorm_quantize_int8."""
+    dev = _one_device(x=x, weight=weight, residual=residual, out=out, scale_out=scale_out, residual_out=residual_out)
+    code = _half_code(x, "x")
+    ldx = _rowmajor(x, "x", x.dtype)
+    M, K = x.shape
+    _vec(weight, "weight", x.dtype, K)
+    ldr = ldo = 0
+    if residual is not None:
+        ldr = _rowmajor(residual, "residual", x.dtype)
+        _shape2(residual, "residual", M, K)
+        if residual_out is None:
+            residual_out = torch.empty((M, (K + 7) // 8 * 8), dtype=x.dtype, device=dev)[:, :K]
+        ldo = _rowmajor(residual_out, "residual_out", x.dtype)
+        _shape2(residual_out, "residual_out", M, K)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if out is None:
+        out = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :K]
+    xs = scale_out if scale_out is not None else torch.empty(M, dtype=torch.float32, device=dev)
+    ldq = _rowmajor(out, "out", torch.int8)
+    _shape2(out, "out", M, K)
+    _vec(xs, "scale_out", torch.float32, M)
+    return (out, xs, residual_out), dev, (_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), code, float(eps), _ptr(out),
+                                          ldq, _ptr(xs), _ptr(residual_out), ldo, M, K)
+
+
+def rmsnorm_quantize_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                          eps: float = 1e-5, out: torch.Tensor | None = None,
+                          scale_out: torch.Tensor | None = None, residual_out: torch.Tensor | None = None):
+    """h = x + residual, RMS norm with `weight`, int8 codes and a scale per row
+    (qg_rmsnorm_quantize_int8) -> (xq, x_scale, h); h is None without a residual.
+    residual_out may be residual or x itself."""
+    r, dev, a = _rmsnorm_args(x, weight, residual, eps, out, scale_out, residual_out)
+    with _on(dev):
+        _check(raw.qg_rmsnorm_quantize_int8(*a, _stream()), "qg_rmsnorm_quantize_int8")
+    return r
+
+
+def dequantize_rowwise_int8(xq: torch.Tensor, x_scale: torch.Tensor, out_dtype: torch.dtype = torch.float16,
+                            out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values xq * x_scale of int8 rows (qg_dequantize_rowwise_int8)."""
+    dev = _one_device(xq=xq, x_scale=x_scale, out=out)
+    if out_dtype not in (torch.float32, *_HALF):
+        raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {out_dtype}")
+    ldq = _rowmajor(xq, "xq", torch.int8)
+    M, K = xq.shape
+    _vec(x_scale, "x_scale", torch.float32, M)
+    if out is None:
+        out = torch.empty((M, (K + 7) // 8 * 8), dtype=out_dtype, device=dev)[:, :K]
+    ldy = _rowmajor(out, "out", out_dtype)
+    _shape2(out, "out", M, K)
+    with _on(dev):
+        _check(raw.qg_dequantize_rowwise_int8(_ptr(xq), ldq, _ptr(x_scale), _ptr(out), _DTYPE_CODE[out_dtype], ldy,
+                                              M, K, _stream()), "qg_dequantize_rowwise_int8")
+    return out
+
+
+class _CKV4Cache(ctypes.Structure):
+    _fields_ = [("k_codes", _vp), ("k_params", _vp), ("v_codes", _vp), ("v_params", _vp), ("num_pages", _i64),
+                ("num_heads", _i64), ("page_size", _i64), ("head_dim", _i64)]
+
+
+class KV4Cache(NamedTuple):
+    """A paged key/value cache in 4 bits (layout: qg_kv4_cache in include/qg.h):
+    codes int32 [num_pages, num_heads, page_size, 8, head_dim / 64] and params
+    (scale, offset) fp16 [num_pages, num_heads, page_size, head_dim / 64, 2]."""
+    k_codes: torch.Tensor
+    k_params: torch.Tensor
+    v_codes: torch.Tensor
+    v_params: torch.Tensor
+
+    @property
+    def num_pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def num_heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k_codes.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return 64 * self.k_codes.shape[4]
+
+
+def kv4_cache(num_pages: int, num_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> KV4Cache:
+    """A zero-filled KV4Cache."""
+    if head_dim not in (64, 128) or page_size <= 0 or page_size % 16:
+        raise ValueError(f"head_dim must be 64 or 128 and page_size a multiple of 16, got {head_dim}, {page_size}")
+    c, p = (num_pages, num_heads, page_size, 8, head_dim // 64), (num_pages, num_heads, page_size, head_dim // 64, 2)
+    z = [torch.zeros(s, dtype=d, device=device) for s, d in ((c, torch.int32), (p, torch.float16)) * 2]
+    return KV4Cache(*z)
+
+
+def _cache_arg(cache: KV4Cache) -> _CKV4Cache:
+    kc = cache.k_codes
+    if kc.dim() != 5 or kc.shape[3] != 8:
+        raise ValueError(f"codes must be [num_pages, num_heads, page_size, 8, head_dim / 64], got {tuple(kc.shape)}")
+    n, h, p, _, g = kc.shape
+    for t, name, dtype, shape in ((kc, "k_codes", torch.int32, (n, h, p, 8, g)),
+                                  (cache.v_codes, "v_codes", torch.int32, (n, h, p, 8, g)),
+                                  (cache.k_params, "k_params", torch.float16, (n, h, p, g, 2)),
+                                  (cache.v_params, "v_params", torch.float16, (n, h, p, g, 2))):
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
+    return _CKV4Cache(kc.data_ptr(), cache.k_params.data_ptr(), cache.v_codes.data_ptr(), cache.v_params.data_ptr(),
+                      n, h, p, 64 * g)
+
+
+def _heads3(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
+    """Token and head strides of a [T, H, D] tensor with unit inner stride."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    # the stride of a dimension of one element is never used
+    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
+
+
+def _slots(slots: torch.Tensor, T: int) -> torch.Tensor:
+    return _vec(slots, "slots", torch.int64, T)
+
+
+def _quantize_kv4_args(k, v, cache, slots):
+    """(tensors to keep, device, the C arguments but the stream) of qg_quantize_kv4."""
+    dev = _one_device(k=k, v=v, slots=slots, **cache._asdict())
+    c = _cache_arg(cache)
+    code = _half_code(k, "k")
+    T = k.shape[0]
+    shape = (T, cache.num_heads, cache.head_dim)
+    ks, vs = _heads3(k, "k", k.dtype, shape), _heads3(v, "v", k.dtype, shape)
+    _slots(slots, T)
+    return (k, v, cache, slots, c), dev, (_ptr(k), *ks, _ptr(v), *vs, code, _ptr(slots), ctypes.byref(c), T)
+
+
+def quantize_kv4(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: torch.Tensor) -> KV4Cache:
+    """Quantize keys and values [T, num_heads, head_dim] into the cache at
+    `slots` int64 [T] (page * page_size + offset; negative: skipped), in place
+    (qg_quantize_kv4)."""
+    _, dev, a = _quantize_kv4_args(k, v, cache, slots)
+    with _on(dev):
+        _check(raw.qg_quantize_kv4(*a, _stream()), "qg_quantize_kv4")
+    return cache
+
+
+def dequantize_kv4(cache: KV4Cache, slots: torch.Tensor, out_dtype: torch.dtype = torch.float16, out=None):
+    """Keys and values [T, num_heads, head_dim] of the tokens at `slots`, zeros at
+    a negative slot (qg_dequantize_kv4).  out: (k, v) to write into."""
+    T, shape = slots.numel(), (slots.numel(), cache.num_heads, cache.head_dim)
+    if out_dtype not in (torch.float32, *_HALF):
+        raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {out_dtype}")
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=out_dtype, device=cache.k_codes.device) for _ in range(2))
+    k, v = out
+    dev = _one_device(slots=slots, k=k, v=v, **cache._asdict())
+    c = _cache_arg(cache)
+    ks, vs = _heads3(k, "out[0]", out_dtype, shape), _heads3(v, "out[1]", out_dtype, shape)
+    _slots(slots, T)
+    with _on(dev):
+        _check(raw.qg_dequantize_kv4(ctypes.byref(c), _ptr(slots), _ptr(k), *ks, _ptr(v), *vs, _DTYPE_CODE[out_dtype],
+                                     T, _stream()), "qg_dequantize_kv4")
+    return k, v
+
+
+def _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal, window, out, lse):
+    """(out, workspace, tensors to keep, device, the C arguments but the stream) of qg_attention_kv4."""
+    dev = _one_device(q=q, block_table=block_table, seq_lens=seq_lens, q_starts=q_starts, out=out, lse=lse,
+                      **cache._asdict())
+    c = _cache_arg(cache)
+    code = _half_code(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, heads_q, head_dim], got {tuple(q.shape)}")
+    T, Hq, _ = q.shape
+    B = seq_lens.numel()
+    shape = (T, Hq, cache.head_dim)
+    qs = _heads3(q, "q", q.dtype, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    os_ = _heads3(out, "out", q.dtype, shape)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
+    ld = _rowmajor(block_table, "block_table", torch.int32)
+    _vec(seq_lens, "seq_lens", torch.int32, B)
+    _vec(q_starts, "q_starts", torch.int32, B + 1)
+    if lse is not None:
+        if lse.dtype is not torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous float32 [{T}, {Hq}]")
+    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+    with _on(dev):
+        need = int(raw.qg_attention_kv4_workspace_size(B, T, Hq, cache.num_heads, cache.head_dim,
+                                                       int(q_starts is not None)))
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    return out, (q, cache, block_table, seq_lens, q_starts, out, lse, ws, c), dev, (
+        _ptr(q), *qs, ctypes.byref(c), _ptr(block_table), ld, _ptr(seq_lens), _ptr(q_starts), scale, int(causal),
+        int(window), _ptr(out), *os_, code, _ptr(lse), B, T, Hq, block_table.shape[1], _ptr(ws), need)
+
+
+def attention_kv4(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                  q_starts: torch.Tensor | None = None, scale: float | None = None, causal: bool = True,
+                  window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of query tokens q [T, heads_q, head_dim], the last ones of B
+    sequences, over the sequences' tokens in the cache (qg_attention_kv4).
+    block_table int32 [B, max_pages], seq_lens int32 [B]; q_starts int32 [B + 1]
+    gives each sequence's rows of q (None: T / B each).  scale defaults to
+    head_dim ** -0.5.  lse float32 [T, heads_q] receives the log-sum-exp."""
+    out, _, dev, a = _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal, window, out, lse)
+    with _on(dev):
+        _check(raw.qg_attention_kv4(*a, _stream()), "qg_attention_kv4")
+    return out
+
+
+# ---------------------------------------------------------------------------
 # Launch plans (qg_plan_*): one call's arguments bound once, launched many times
 # ---------------------------------------------------------------------------
 class Plan:
@@ -562,14 +842,17 @@ class Plan:
     plan) until launches issued on other streams have finished.  close() is
     for one thread; launch() may be called from several."""
 
-    __slots__ = ("_h", "_keep", "out")
+    __slots__ = ("_h", "_keep", "out", "_dev")
 
-    def __init__(self, handle: int, keep: tuple, out):
-        self._h, self._keep, self.out = handle, keep, out
+    def __init__(self, handle: int, keep: tuple, out, dev: torch.device | None = None):
+        self._h, self._keep, self.out, self._dev = handle, keep, out, dev
 
     def launch(self, stream=None) -> None:
         """Issue the call on `stream` (a torch.cuda.Stream or a raw handle;
         default: the current stream)."""
+        if self._dev is not None and self._dev.index != torch.cuda.current_device():
+            with torch.cuda.device(self._dev):
+                return self.launch(stream)
         s = _stream() if stream is None else getattr(stream, "cuda_stream", stream)
         st = raw.qg_plan_launch(self._h, s)
         if st != QG_OK:
@@ -587,10 +870,10 @@ class Plan:
         self.close()
 
 
-def _new_plan(fn, args, keep, out, where: str) -> Plan:
+def _new_plan(fn, args, keep, out, where: str, dev: torch.device | None = None) -> Plan:
     h = ctypes.c_void_p()
     _check(fn(ctypes.byref(h), *args), where)
-    return Plan(h.value, keep, out)
+    return Plan(h.value, keep, out, dev)
 
 
 def _plan_workspace(workspace):
@@ -634,3 +917,28 @@ def plan_gemm_w4a16(x: torch.Tensor, qweight: torch.Tensor, scale: torch.Tensor,
     flags = QG_FLAG_STATIC_WEIGHTS if static_weights else 0
     return _new_plan(raw.qg_plan_gemm_w4a16, a + (flags,), (x, qweight, scale, zero, bias, y, wst), y,
                      "qg_plan_gemm_w4a16")
+
+
+def plan_rmsnorm_quantize_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                               eps: float = 1e-5, out: torch.Tensor | None = None,
+                               scale_out: torch.Tensor | None = None,
+                               residual_out: torch.Tensor | None = None) -> Plan:
+    """qg_plan_rmsnorm_quantize_int8: rmsnorm_quantize_int8 bound to its operands and outputs."""
+    r, dev, a = _rmsnorm_args(x, weight, residual, eps, out, scale_out, residual_out)
+    return _new_plan(raw.qg_plan_rmsnorm_quantize_int8, a, (x, weight, residual, *r), r,
+                     "qg_plan_rmsnorm_quantize_int8", dev)
+
+
+def plan_quantize_kv4(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: torch.Tensor) -> Plan:
+    """qg_plan_quantize_kv4: quantize_kv4 bound to its operands and cache."""
+    keep, dev, a = _quantize_kv4_args(k, v, cache, slots)
+    return _new_plan(raw.qg_plan_quantize_kv4, a, keep, cache, "qg_plan_quantize_kv4", dev)
+
+
+def plan_attention_kv4(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                       q_starts: torch.Tensor | None = None, scale: float | None = None, causal: bool = True,
+                       window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None) -> Plan:
+    """qg_plan_attention_kv4: attention_kv4 bound to its operands, output and a
+    workspace of the plan's own (launches of one plan must not overlap)."""
+    out, keep, dev, a = _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal, window, out, lse)
+    return _new_plan(raw.qg_plan_attention_kv4, a, keep, out, "qg_plan_attention_kv4", dev)

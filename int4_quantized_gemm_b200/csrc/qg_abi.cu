@@ -5,7 +5,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -16,6 +18,7 @@
 #include "../../include/qg.h"
 #include "qg_device.cuh"
 #include "qg_internal.h"
+#include "qg_kv4.cuh"
 
 #define QG_VERSION 100  // 0.1.0
 
@@ -171,6 +174,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxKInt8 = 133144;  // 2^31 / 127^2: int32 accumulation stays exact
+constexpr int kMaxSequences = 4096;    // per attention call: their lengths are scanned in shared memory
 constexpr int64_t kMaxKZp = 131071;    // 2^31 / 128^2 - 1: the same with codes in [-128, 127]
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -322,19 +326,24 @@ size_t qg_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
 qg_status qg_check_device_errors(qg_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   QG_TRY(check_cuda(cudaStreamSynchronize(s), "cudaStreamSynchronize"));
-  unsigned long long words[6] = {read_clear_status_quantize(s), read_clear_status_w8a8(s),
+  unsigned long long words[8] = {read_clear_status_quantize(s), read_clear_status_w8a8(s),
                                  read_clear_status_wonly(s), read_clear_status_decode(s),
-                                 read_clear_status_pair(s), read_clear_status_wide(s)};
+                                 read_clear_status_pair(s), read_clear_status_wide(s),
+                                 read_clear_status_kv4(s), read_clear_status_attn(s)};
   QG_TRY(check_cuda(cudaGetLastError(), "reading device status"));
-  static const char* names[6] = {"quantize", "w8a8", "weight-only", "decode", "w8a8 pair", "weight-only wide"};
-  for (int i = 0; i < 6; ++i) {
+  static const char* names[8] = {"quantize", "w8a8", "weight-only", "decode", "w8a8 pair", "weight-only wide",
+                                 "4-bit cache", "attention"};
+  for (int i = 0; i < 8; ++i) {
     if (words[i] != 0) {
       const unsigned code = (unsigned)(words[i] & 0xFF);
       const unsigned site = (unsigned)((words[i] >> 8) & 0xFFFF);
       const unsigned long long block = words[i] >> 24;
-      const qg_status st = code == kDevTimeout ? QG_ERR_TIMEOUT : code == kDevDebugCheck ? QG_ERR_DEBUG_CHECK : QG_ERR_CUDA;
+      const qg_status st = code == kDevTimeout      ? QG_ERR_TIMEOUT
+                           : code == kDevDebugCheck ? QG_ERR_DEBUG_CHECK
+                           : code == kDevBadArg     ? QG_ERR_INVALID_ARG
+                                                    : QG_ERR_CUDA;
       return fail(st, "%s kernel: device status code %u at %s site %u, block %llu", names[i], code,
-                  code == kDevDebugCheck ? "check" : "wait", site, block);
+                  code == kDevDebugCheck ? "check" : code == kDevBadArg ? "index" : "wait", site, block);
     }
   }
   return QG_OK;
@@ -683,12 +692,191 @@ qg_status qg_gemm_w4a16_act(const void* x, int64_t ldx, const int32_t* qweight, 
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Norm, 4-bit cache and attention
+// ---------------------------------------------------------------------------
+namespace {
+
+qg_status check_half_dtype(int dtype, const char* name) {
+  if (dtype != QG_F16 && dtype != QG_BF16) return fail(QG_ERR_INVALID_ARG, "%s: dtype %d is not QG_F16 or QG_BF16", name, dtype);
+  return QG_OK;
+}
+
+qg_status check_cache(const qg_kv4_cache* c, KV4* out) {
+  if (!c) return fail(QG_ERR_INVALID_ARG, "cache is NULL");
+  if (c->num_pages < 0 || c->num_heads < 1 || c->page_size < 1)
+    return fail(QG_ERR_INVALID_ARG, "cache: num_pages=%lld num_heads=%lld page_size=%lld", (long long)c->num_pages, (long long)c->num_heads, (long long)c->page_size);
+  if (c->head_dim != 64 && c->head_dim != 128) return fail(QG_ERR_UNSUPPORTED, "head_dim %lld: only 64 and 128 are implemented", (long long)c->head_dim);
+  if (c->page_size % 16 != 0) return fail(QG_ERR_INVALID_ARG, "page_size %lld is not a multiple of 16", (long long)c->page_size);
+  if (c->num_pages >= kMaxDim || c->page_size > 65536 || c->num_heads > 65536) return fail(QG_ERR_UNSUPPORTED, "cache: num_pages >= 2^31, or page_size or num_heads above 65536");
+  if (c->num_pages > 0) {
+    QG_TRY(check_vec(c->k_codes, 16, "k_codes", false));
+    QG_TRY(check_vec(c->k_params, 16, "k_params", false));
+    QG_TRY(check_vec(c->v_codes, 16, "v_codes", false));
+    QG_TRY(check_vec(c->v_params, 16, "v_params", false));
+  }
+  out->codes[0] = reinterpret_cast<uint32_t*>(c->k_codes);
+  out->codes[1] = reinterpret_cast<uint32_t*>(c->v_codes);
+  out->params[0] = static_cast<uint32_t*>(c->k_params);
+  out->params[1] = static_cast<uint32_t*>(c->v_params);
+  out->pages = c->num_pages;
+  out->heads = (int)c->num_heads;
+  out->page_size = (int)c->page_size;
+  out->dim = (int)c->head_dim;
+  return QG_OK;
+}
+
+// [tokens, heads, dim] with unit inner stride, rows on 16-byte boundaries
+qg_status check_rows3(const void* p, int64_t st, int64_t sh, int elem, const char* name) {
+  if (!p) return fail(QG_ERR_INVALID_ARG, "%s is NULL", name);
+  if (st < 0 || sh < 0) return fail(QG_ERR_INVALID_ARG, "%s: negative stride", name);
+  if (!aligned(p, 16)) return fail(QG_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
+  if ((st * elem) % 16 != 0 || (sh * elem) % 16 != 0) return fail(QG_ERR_ALIGNMENT, "%s: strides are not multiples of 16 bytes", name);
+  return QG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qg_status qg_rmsnorm_quantize_int8(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                   int dtype, float eps, int8_t* xq, int64_t ldxq, float* x_scale,
+                                   void* residual_out, int64_t ldro, int64_t M, int64_t K, qg_stream_t stream) {
+  QG_TRY(check_dims(M, 0, K));
+  QG_TRY(check_half_dtype(dtype, "x"));
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(QG_ERR_INVALID_ARG, "eps %g is not a positive number", (double)eps);
+  if (K == 0) return fail(QG_ERR_INVALID_ARG, "K=0: a norm needs at least one column");
+  if ((residual == nullptr) != (residual_out == nullptr)) return fail(QG_ERR_INVALID_ARG, "residual and residual_out go together");
+  if (M == 0) return QG_OK;
+  QG_TRY(check_matrix(x, ldx, K, 2, "x"));
+  if (residual) {
+    QG_TRY(check_matrix(residual, ldr, K, 2, "residual"));
+    QG_TRY(check_matrix(residual_out, ldro, K, 2, "residual_out"));
+  }
+  QG_TRY(check_vec(weight, 16, "weight", false));
+  QG_TRY(check_matrix(xq, ldxq, K, 1, "xq"));
+  QG_TRY(check_vec(x_scale, 4, "x_scale", false));
+  QG_TRY(check_device());
+  return launch_rmsnorm_quantize(x, ldx, residual, ldr, weight, dtype, eps, xq, ldxq, x_scale, residual_out, ldro, M,
+                                 K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qg_status qg_dequantize_rowwise_int8(const int8_t* xq, int64_t ldxq, const float* x_scale, void* y, int y_dtype,
+                                     int64_t ldy, int64_t M, int64_t K, qg_stream_t stream) {
+  QG_TRY(check_dims(M, 0, K));
+  if (y_dtype < QG_F32 || y_dtype > QG_BF16) return fail(QG_ERR_INVALID_ARG, "unknown output dtype %d", y_dtype);
+  if (M == 0 || K == 0) return QG_OK;
+  QG_TRY(check_matrix(xq, ldxq, K, 1, "xq"));
+  QG_TRY(check_vec(x_scale, 4, "x_scale", false));
+  QG_TRY(check_matrix(y, ldy, K, y_dtype == QG_F32 ? 4 : 2, "y"));
+  QG_TRY(check_device());
+  return launch_dequantize_rowwise(xq, ldxq, x_scale, y, y_dtype, ldy, M, K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qg_status qg_quantize_kv4(const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                          int64_t v_stride_h, int dtype, const int64_t* slots, const qg_kv4_cache* cache, int64_t T,
+                          qg_stream_t stream) {
+  QG_TRY(check_dims(T, 0, 0));
+  QG_TRY(check_half_dtype(dtype, "k, v"));
+  KV4 c;
+  QG_TRY(check_cache(cache, &c));
+  if (T == 0) return QG_OK;
+  QG_TRY(check_rows3(k, k_stride_t, k_stride_h, 2, "k"));
+  QG_TRY(check_rows3(v, v_stride_t, v_stride_h, 2, "v"));
+  QG_TRY(check_vec(slots, 8, "slots", false));
+  QG_TRY(check_device());
+  return launch_quantize_kv4(k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, dtype, slots, c, T,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+qg_status qg_dequantize_kv4(const qg_kv4_cache* cache, const int64_t* slots, void* k, int64_t k_stride_t,
+                            int64_t k_stride_h, void* v, int64_t v_stride_t, int64_t v_stride_h, int dtype, int64_t T,
+                            qg_stream_t stream) {
+  QG_TRY(check_dims(T, 0, 0));
+  if (dtype < QG_F32 || dtype > QG_BF16) return fail(QG_ERR_INVALID_ARG, "unknown output dtype %d", dtype);
+  KV4 c;
+  QG_TRY(check_cache(cache, &c));
+  if (T == 0) return QG_OK;
+  const int es = dtype == QG_F32 ? 4 : 2;
+  QG_TRY(check_rows3(k, k_stride_t, k_stride_h, es, "k"));
+  QG_TRY(check_rows3(v, v_stride_t, v_stride_h, es, "v"));
+  QG_TRY(check_vec(slots, 8, "slots", false));
+  QG_TRY(check_device());
+  return launch_dequantize_kv4(c, slots, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, dtype, T,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t qg_attention_kv4_workspace_size(int64_t B, int64_t T, int64_t heads_q, int64_t num_heads, int64_t head_dim,
+                                       int ragged) {
+  if (B <= 0 || T <= 0 || heads_q <= 0 || num_heads <= 0 || heads_q % num_heads != 0 ||
+      (head_dim != 64 && head_dim != 128) || T * heads_q >= kMaxDim)
+    return 0;
+  return attention_kv4_workspace(B, T, heads_q, num_heads, head_dim, ragged != 0);
+}
+
+qg_status qg_attention_kv4(const void* q, int64_t q_stride_t, int64_t q_stride_h, const qg_kv4_cache* cache,
+                           const int32_t* block_table, int64_t ld_table, const int32_t* seq_lens,
+                           const int32_t* q_starts, float scale, int causal, int64_t window, void* out,
+                           int64_t out_stride_t, int64_t out_stride_h, int dtype, float* lse, int64_t B, int64_t T,
+                           int64_t heads_q, int64_t max_pages, void* workspace, size_t workspace_bytes,
+                           qg_stream_t stream) {
+  QG_TRY(check_dims(B, T, heads_q));
+  QG_TRY(check_half_dtype(dtype, "q"));
+  Attn4 a = {};
+  QG_TRY(check_cache(cache, &a.cache));
+  if (heads_q < 1 || heads_q % a.cache.heads != 0) return fail(QG_ERR_INVALID_ARG, "heads_q %lld is not a multiple of the cache's %d heads", (long long)heads_q, a.cache.heads);
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QG_ERR_INVALID_ARG, "scale %g is not a positive number", (double)scale);
+  if (window < 0 || max_pages < 0) return fail(QG_ERR_INVALID_ARG, "negative window or max_pages");
+  if (B > kMaxSequences) return fail(QG_ERR_UNSUPPORTED, "B=%lld sequences: at most %d", (long long)B, kMaxSequences);
+  if (T * heads_q >= kMaxDim || max_pages * a.cache.page_size >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "T * heads_q or max_pages * page_size >= 2^31");
+  if (B > 0 && !q_starts && T % B != 0) return fail(QG_ERR_INVALID_ARG, "T=%lld is not a multiple of B=%lld (pass q_starts)", (long long)T, (long long)B);
+  if (B == 0 || T == 0) return QG_OK;
+  QG_TRY(check_rows3(q, q_stride_t, q_stride_h, 2, "q"));
+  QG_TRY(check_rows3(out, out_stride_t, out_stride_h, 2, "out"));
+  QG_TRY(check_vec(block_table, 4, "block_table", max_pages == 0));
+  if (ld_table < max_pages) return fail(QG_ERR_INVALID_ARG, "block_table: leading dimension %lld < %lld", (long long)ld_table, (long long)max_pages);
+  QG_TRY(check_vec(seq_lens, 4, "seq_lens", false));
+  QG_TRY(check_vec(q_starts, 4, "q_starts", true));
+  QG_TRY(check_vec(lse, 4, "lse", true));
+  const size_t need = attention_kv4_workspace(B, T, heads_q, a.cache.heads, a.cache.dim, q_starts != nullptr);
+  if (need > 0) {
+    if (!workspace) return fail(QG_ERR_INVALID_ARG, "workspace is NULL (%zu bytes needed)", need);
+    if (workspace_bytes < need) return fail(QG_ERR_INVALID_ARG, "workspace of %zu bytes: %zu needed", workspace_bytes, need);
+    if (!aligned(workspace, 16)) return fail(QG_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  }
+  QG_TRY(check_device());
+  a.q = q;
+  a.out = out;
+  a.q_st = q_stride_t;
+  a.q_sh = q_stride_h;
+  a.o_st = out_stride_t;
+  a.o_sh = out_stride_h;
+  a.lse = lse;
+  a.table = block_table;
+  a.table_ld = ld_table;
+  a.seq_lens = seq_lens;
+  a.q_starts = q_starts;
+  a.n_uniform = q_starts ? 0 : (int)(T / B);
+  a.B = (int)B;
+  a.T = (int)T;
+  a.heads_q = (int)heads_q;
+  a.group = (int)heads_q / a.cache.heads;
+  a.max_pages = (int)max_pages;
+  a.scale = scale;
+  a.causal = causal != 0;
+  a.window = (int)std::min<int64_t>(window, kMaxDim - 1);
+  a.dtype = dtype;
+  return launch_attention_kv4(a, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // Launch plans: the bound arguments of one entry point, replayed on a stream.
 // A launch goes through the same internal entry as the direct call, argument
 // checks included, so both return the same status for the same arguments.
 // ---------------------------------------------------------------------------
 struct qg_plan {
-  enum Op { kQuantize, kW8A8, kW8A16, kW4A16 } op;
+  enum Op { kQuantize, kW8A8, kW8A16, kW4A16, kNorm, kQuantizeKV4, kAttentionKV4 } op;
   const void* x;     // x (fp16) or xq (int8)
   int64_t ldx;
   const void* w;     // wq, or qweight
@@ -703,6 +891,21 @@ struct qg_plan {
   void* workspace;
   size_t workspace_bytes;
   unsigned flags;
+  // norm: x, ldx, weight in w, xq in y / ldy, x_scale in s0, M, K; and
+  const void* residual;
+  int64_t ldr;
+  void* residual_out;
+  int64_t ldro;
+  float eps;
+  // cache writer: k in x, v in w, M tokens; attention: q in x, out in y; and
+  qg_kv4_cache cache;
+  int64_t strides[4];  // token and head strides of k and v, or of q and out
+  const int64_t* slots;
+  const int32_t *table, *seq_lens, *q_starts;
+  int64_t ld_table, window, B, heads_q, max_pages;
+  float scale;
+  int causal;
+  float* lse;
 };
 
 namespace {
@@ -805,6 +1008,82 @@ qg_status qg_plan_gemm_w4a16(qg_plan** plan, const void* x, int64_t ldx, const i
   return new_plan(plan, p);
 }
 
+qg_status qg_plan_rmsnorm_quantize_int8(qg_plan** plan, const void* x, int64_t ldx, const void* residual,
+                                        int64_t ldr, const void* weight, int dtype, float eps, int8_t* xq,
+                                        int64_t ldxq, float* x_scale, void* residual_out, int64_t ldro, int64_t M,
+                                        int64_t K) {
+  qg_plan p = {};
+  p.op = qg_plan::kNorm;
+  p.x = x;
+  p.ldx = ldx;
+  p.residual = residual;
+  p.ldr = ldr;
+  p.w = weight;
+  p.y_dtype = dtype;
+  p.eps = eps;
+  p.y = xq;
+  p.ldy = ldxq;
+  p.s0 = x_scale;
+  p.residual_out = residual_out;
+  p.ldro = ldro;
+  p.M = M;
+  p.K = K;
+  return new_plan(plan, p);
+}
+
+qg_status qg_plan_quantize_kv4(qg_plan** plan, const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+                               int64_t v_stride_t, int64_t v_stride_h, int dtype, const int64_t* slots,
+                               const qg_kv4_cache* cache, int64_t T) {
+  if (!cache) return fail(QG_ERR_INVALID_ARG, "cache is NULL");
+  qg_plan p = {};
+  p.op = qg_plan::kQuantizeKV4;
+  p.x = k;
+  p.w = v;
+  p.strides[0] = k_stride_t;
+  p.strides[1] = k_stride_h;
+  p.strides[2] = v_stride_t;
+  p.strides[3] = v_stride_h;
+  p.y_dtype = dtype;
+  p.slots = slots;
+  p.cache = *cache;
+  p.M = T;
+  return new_plan(plan, p);
+}
+
+qg_status qg_plan_attention_kv4(qg_plan** plan, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                const qg_kv4_cache* cache, const int32_t* block_table, int64_t ld_table,
+                                const int32_t* seq_lens, const int32_t* q_starts, float scale, int causal,
+                                int64_t window, void* out, int64_t out_stride_t, int64_t out_stride_h, int dtype,
+                                float* lse, int64_t B, int64_t T, int64_t heads_q, int64_t max_pages,
+                                void* workspace, size_t workspace_bytes) {
+  if (!cache) return fail(QG_ERR_INVALID_ARG, "cache is NULL");
+  qg_plan p = {};
+  p.op = qg_plan::kAttentionKV4;
+  p.x = q;
+  p.y = out;
+  p.strides[0] = q_stride_t;
+  p.strides[1] = q_stride_h;
+  p.strides[2] = out_stride_t;
+  p.strides[3] = out_stride_h;
+  p.y_dtype = dtype;
+  p.cache = *cache;
+  p.table = block_table;
+  p.ld_table = ld_table;
+  p.seq_lens = seq_lens;
+  p.q_starts = q_starts;
+  p.scale = scale;
+  p.causal = causal;
+  p.window = window;
+  p.lse = lse;
+  p.B = B;
+  p.M = T;
+  p.heads_q = heads_q;
+  p.max_pages = max_pages;
+  p.workspace = workspace;
+  p.workspace_bytes = workspace_bytes;
+  return new_plan(plan, p);
+}
+
 qg_status qg_plan_launch(const qg_plan* p, qg_stream_t stream) {
   if (!p) return fail(QG_ERR_INVALID_ARG, "plan is NULL");
   switch (p->op) {
@@ -824,6 +1103,19 @@ qg_status qg_plan_launch(const qg_plan* p, qg_stream_t stream) {
       return gemm_w4a16(p->x, p->ldx, static_cast<const int32_t*>(p->w), p->s0, p->s1, p->group, p->bias, p->y,
                         p->ldy, p->M, p->N, p->K, p->workspace, p->workspace_bytes, QG_ACT_NONE, p->flags,
                         stream);
+    case qg_plan::kNorm:
+      return qg_rmsnorm_quantize_int8(p->x, p->ldx, p->residual, p->ldr, p->w, p->y_dtype, p->eps,
+                                      static_cast<int8_t*>(p->y), p->ldy,
+                                      static_cast<float*>(const_cast<void*>(p->s0)), p->residual_out, p->ldro, p->M,
+                                      p->K, stream);
+    case qg_plan::kQuantizeKV4:
+      return qg_quantize_kv4(p->x, p->strides[0], p->strides[1], p->w, p->strides[2], p->strides[3], p->y_dtype,
+                             p->slots, &p->cache, p->M, stream);
+    case qg_plan::kAttentionKV4:
+      return qg_attention_kv4(p->x, p->strides[0], p->strides[1], &p->cache, p->table, p->ld_table, p->seq_lens,
+                              p->q_starts, p->scale, p->causal, p->window, p->y, p->strides[2], p->strides[3],
+                              p->y_dtype, p->lse, p->B, p->M, p->heads_q, p->max_pages, p->workspace,
+                              p->workspace_bytes, stream);
   }
   return fail(QG_ERR_INVALID_ARG, "plan of unknown kind");
 }

@@ -181,6 +181,23 @@ qg_status launch_wonly_wide(bool w4, const void* x, int64_t ldx, const void* w, 
                             int64_t ldy, int64_t M, int64_t N, int64_t K, cudaStream_t s, int act, bool sym,
                             unsigned flags, int bn_force);
 unsigned long long read_clear_status_wide(cudaStream_t s);
+// RMS norm with residual addition and int8 codes per row; the int8 row reader (qg_norm.cu).
+qg_status launch_rmsnorm_quantize(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                  int dtype, float eps, int8_t* xq, int64_t ldq, float* xs, void* res_out,
+                                  int64_t ldo, int64_t M, int64_t K, cudaStream_t s);
+qg_status launch_dequantize_rowwise(const int8_t* xq, int64_t ldq, const float* xs, void* y, int dtype, int64_t ldy,
+                                    int64_t M, int64_t K, cudaStream_t s);
+// The paged 4-bit cache: writer, reader (qg_kv4.cu) and attention (qg_kv4.cuh describes the structs).
+struct KV4;
+struct Attn4;
+qg_status launch_quantize_kv4(const void* k, int64_t kst, int64_t ksh, const void* v, int64_t vst, int64_t vsh,
+                              int dtype, const int64_t* slots, const KV4& cache, int64_t T, cudaStream_t s);
+qg_status launch_dequantize_kv4(const KV4& cache, const int64_t* slots, void* k, int64_t kst, int64_t ksh, void* v,
+                                int64_t vst, int64_t vsh, int dtype, int64_t T, cudaStream_t s);
+qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s);
+size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t dim, bool ragged);
+unsigned long long read_clear_status_kv4(cudaStream_t s);
+unsigned long long read_clear_status_attn(cudaStream_t s);
 // Y = bias (or 0) for the empty sum K == 0.
 qg_status launch_fill_bias(const float* bias, void* y, int dtype, int64_t ldy, int64_t M,
                            int64_t N, cudaStream_t s, int act = 0);
