@@ -326,14 +326,15 @@ size_t qg_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
 qg_status qg_check_device_errors(qg_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   QG_TRY(check_cuda(cudaStreamSynchronize(s), "cudaStreamSynchronize"));
-  unsigned long long words[8] = {read_clear_status_quantize(s), read_clear_status_w8a8(s),
+  unsigned long long words[9] = {read_clear_status_quantize(s), read_clear_status_w8a8(s),
                                  read_clear_status_wonly(s), read_clear_status_decode(s),
                                  read_clear_status_pair(s), read_clear_status_wide(s),
-                                 read_clear_status_kv4(s), read_clear_status_attn(s)};
+                                 read_clear_status_kv4(s), read_clear_status_attn(s),
+                                 read_clear_status_prompt(s)};
   QG_TRY(check_cuda(cudaGetLastError(), "reading device status"));
-  static const char* names[8] = {"quantize", "w8a8", "weight-only", "decode", "w8a8 pair", "weight-only wide",
-                                 "4-bit cache", "attention"};
-  for (int i = 0; i < 8; ++i) {
+  static const char* names[9] = {"quantize", "w8a8", "weight-only", "decode", "w8a8 pair", "weight-only wide",
+                                 "4-bit cache", "attention decode", "attention"};
+  for (int i = 0; i < 9; ++i) {
     if (words[i] != 0) {
       const unsigned code = (unsigned)(words[i] & 0xFF);
       const unsigned site = (unsigned)((words[i] >> 8) & 0xFFFF);
@@ -707,7 +708,7 @@ qg_status check_cache(const qg_kv4_cache* c, KV4* out) {
     return fail(QG_ERR_INVALID_ARG, "cache: num_pages=%lld num_heads=%lld page_size=%lld", (long long)c->num_pages, (long long)c->num_heads, (long long)c->page_size);
   if (c->head_dim != 64 && c->head_dim != 128) return fail(QG_ERR_UNSUPPORTED, "head_dim %lld: only 64 and 128 are implemented", (long long)c->head_dim);
   if (c->page_size % 16 != 0) return fail(QG_ERR_INVALID_ARG, "page_size %lld is not a multiple of 16", (long long)c->page_size);
-  if (c->num_pages >= kMaxDim || c->page_size > 65536 || c->num_heads > 65536) return fail(QG_ERR_UNSUPPORTED, "cache: num_pages >= 2^31, or page_size or num_heads above 65536");
+  if (c->num_pages >= kMaxDim || c->page_size > 65536 || c->num_heads > 65535) return fail(QG_ERR_UNSUPPORTED, "cache: num_pages >= 2^31, page_size above 65536 or num_heads above 65535");
   if (c->num_pages > 0) {
     QG_TRY(check_vec(c->k_codes, 16, "k_codes", false));
     QG_TRY(check_vec(c->k_params, 16, "k_params", false));
@@ -828,6 +829,7 @@ qg_status qg_attention_kv4(const void* q, int64_t q_stride_t, int64_t q_stride_h
   if (window < 0 || max_pages < 0) return fail(QG_ERR_INVALID_ARG, "negative window or max_pages");
   if (B > kMaxSequences) return fail(QG_ERR_UNSUPPORTED, "B=%lld sequences: at most %d", (long long)B, kMaxSequences);
   if (T * heads_q >= kMaxDim || max_pages * a.cache.page_size >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "T * heads_q or max_pages * page_size >= 2^31");
+  if (B * a.cache.heads * (max_pages * a.cache.page_size / 64 + 1) >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "B * num_heads * max_pages * page_size / 64 >= 2^31");
   if (B > 0 && !q_starts && T % B != 0) return fail(QG_ERR_INVALID_ARG, "T=%lld is not a multiple of B=%lld (pass q_starts)", (long long)T, (long long)B);
   if (B == 0 || T == 0) return QG_OK;
   QG_TRY(check_rows3(q, q_stride_t, q_stride_h, 2, "q"));

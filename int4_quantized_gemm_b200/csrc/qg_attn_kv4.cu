@@ -14,12 +14,12 @@
 
 namespace qg {
 
-static __device__ unsigned long long g_status_attn;
+static __device__ unsigned long long g_status_prompt;
 
-unsigned long long read_clear_status_attn(cudaStream_t s) {
+unsigned long long read_clear_status_prompt(cudaStream_t s) {
   unsigned long long v = 0, z = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_status_attn, sizeof(v), 0, cudaMemcpyDeviceToHost, s);
-  cudaMemcpyToSymbolAsync(g_status_attn, &z, sizeof(z), 0, cudaMemcpyHostToDevice, s);
+  cudaMemcpyFromSymbolAsync(&v, g_status_prompt, sizeof(v), 0, cudaMemcpyDeviceToHost, s);
+  cudaMemcpyToSymbolAsync(g_status_prompt, &z, sizeof(z), 0, cudaMemcpyHostToDevice, s);
   cudaStreamSynchronize(s);
   return v;
 }
@@ -27,12 +27,12 @@ unsigned long long read_clear_status_attn(cudaStream_t s) {
 namespace {
 
 __device__ __forceinline__ void report_bad(uint32_t site) {
-  atomicCAS(&g_status_attn, 0ull,
+  atomicCAS(&g_status_prompt, 0ull,
             (unsigned long long)kDevBadArg | ((unsigned long long)site << 8) | ((unsigned long long)blockIdx.x << 24));
 }
 
 template <typename T, int DIM>
-__global__ void __launch_bounds__(128) attention_kv4_simple(Attn4 a) {
+__global__ void __launch_bounds__(128) attention_kv4_simple(Attn4 a, int min_rows) {
   constexpr int C = DIM / 32;
   pdl_trigger();
   pdl_wait();
@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(128) attention_kv4_simple(Attn4 a) {
   }
   attn4_sequence(a, b, first, n, len);
   if (t < first || t >= first + n) return;  // a row of no sequence
+  if (n * a.group < min_rows) return;       // the decode kernel's
   const int pos = len - n + (t - first);
   const int end = a.causal ? min(len, pos + 1) : len;
   const int begin = a.window > 0 ? max(0, pos - a.window + 1) : 0;
@@ -113,18 +114,34 @@ __global__ void __launch_bounds__(128) attention_kv4_simple(Attn4 a) {
 
 }  // namespace
 
-size_t attention_kv4_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, bool) { return 0; }
+// Rows (query tokens x head group) that the decode kernel takes, in tiles of 8;
+// 0: none.  Ragged calls give it the sequences of one tile's size or less.
+static int decode_tiles(int64_t n, int64_t group, bool ragged) {
+  const int64_t rows = ragged ? group : n * group;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
+}
 
-qg_status launch_attention_kv4(const Attn4& a, void*, cudaStream_t s) {
+size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t dim, bool ragged) {
+  const int nt = decode_tiles(T / B, heads_q / heads, ragged);
+  return nt ? attention_kv4_decode_workspace(B, dim, nt) : 0;
+}
+
+qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s) {
+  const int nt = decode_tiles(a.n_uniform, a.group, a.q_starts != nullptr);
+  if (nt) {
+    const qg_status st = launch_attention_kv4_decode(a, nt, workspace, s);
+    if (st != QG_OK || !a.q_starts) return st;
+  }
   const int64_t items = (int64_t)a.T * a.heads_q;
+  const int min_rows = 8 * nt + 1;
   LaunchCfg lc((unsigned)((items + 3) / 4), 128, 0, s);
   cudaError_t e;
   if (a.dtype == QG_F16)
-    e = a.cache.dim == 64 ? cudaLaunchKernelEx(&lc.cfg, attention_kv4_simple<__half, 64>, a)
-                          : cudaLaunchKernelEx(&lc.cfg, attention_kv4_simple<__half, 128>, a);
+    e = a.cache.dim == 64 ? cudaLaunchKernelEx(&lc.cfg, attention_kv4_simple<__half, 64>, a, min_rows)
+                          : cudaLaunchKernelEx(&lc.cfg, attention_kv4_simple<__half, 128>, a, min_rows);
   else
-    e = a.cache.dim == 64 ? cudaLaunchKernelEx(&lc.cfg, attention_kv4_simple<__nv_bfloat16, 64>, a)
-                          : cudaLaunchKernelEx(&lc.cfg, attention_kv4_simple<__nv_bfloat16, 128>, a);
+    e = a.cache.dim == 64 ? cudaLaunchKernelEx(&lc.cfg, attention_kv4_simple<__nv_bfloat16, 64>, a, min_rows)
+                          : cudaLaunchKernelEx(&lc.cfg, attention_kv4_simple<__nv_bfloat16, 128>, a, min_rows);
   return check_cuda(e, "attention_kv4 launch");
 }
 

@@ -197,7 +197,11 @@ qg_status launch_dequantize_kv4(const KV4& cache, const int64_t* slots, void* k,
 qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s);
 size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t dim, bool ragged);
 unsigned long long read_clear_status_kv4(cudaStream_t s);
+// Sequences of at most 8 nt query rows per KV head (qg_attn_kv4_decode.cu).
+qg_status launch_attention_kv4_decode(const Attn4& a, int nt, void* workspace, cudaStream_t s);
+size_t attention_kv4_decode_workspace(int64_t B, int64_t dim, int nt);
 unsigned long long read_clear_status_attn(cudaStream_t s);
+unsigned long long read_clear_status_prompt(cudaStream_t s);
 // Y = bias (or 0) for the empty sum K == 0.
 qg_status launch_fill_bias(const float* bias, void* y, int dtype, int64_t ldy, int64_t M,
                            int64_t N, cudaStream_t s, int act = 0);
