@@ -7,14 +7,19 @@
 // decides the time is therefore the instructions per code, and the codes are
 // never dequantized one by one:
 //   score_j = sum_g [ s_jg (q_g . c_jg) + o_jg sum(q_g) ]
-//   out     = sum_j p_j (s_jg c_j + o_jg) = sum_j (p_j s_jg) c_j + sum_j p_j o_jg
+//   out     = sum_j p_j (s_jg c_j + o_jg) = sum_j (p_j s_jg) (c_j - 8) + sum_j p_j (o_jg + 8 s_jg)
 // (g: group of 64 channels; s, o: its scale and offset; c: codes).  The products
 // run on the codes themselves.  A nibble masked into the low bits of a half is
 // the fp16 subnormal c 2^-24 (or, four bits up, 16 c 2^-24), exact on the tensor
 // cores: two codes cost one mask, with one shift per four.  Queries are scaled
 // by a power of two to fp16 (1/16 of it where they meet a nibble four bits up),
 // scale and offset enter per token and group in binary32.  p s is rounded to
-// fp16 under a power of two kappa that keeps the largest near 2^8.
+// fp16 under a power of two kappa (a shift of the running maximum) that keeps
+// the largest near 2^8.  Codes are
+// taken from their middle (a second product with the constant -8, cheaper than
+// changing the codes) because values have either sign: without it the sum over
+// n keys is large against the result and its truncation shows (0.0013 instead
+// of 0.0003 relative error at 131071 keys).
 //
 // mma.m16n8k16 with keys (16 tokens) or channels (16 of V^T) as its rows and up
 // to 8 query rows as its columns: the accumulators of q.c and of the output
@@ -54,6 +59,7 @@ namespace {
 constexpr int kChunk = 64;   // tokens per ring stage
 constexpr int kWarps = 8;    // workers per CTA
 constexpr int kStages = 2;
+constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // fp16x2: -8 2^-24, -128 2^-24
 
 // device status sites
 enum : uint32_t { kSiteSequence = 1, kSitePage = 2, kSiteWait = 3 };
@@ -75,6 +81,22 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// max of each signed 16-bit half
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -287,9 +309,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   float sigma[NT][2];              // scale log2(e) 2^24 over the queries' power of two
   float m[NT][2], l[NT][2];        // running maximum (before sigma) and sum
   float ob[NT][2][G];              // sum p o
-  float o[NT][G][4][4];            // sum (p s kappa) c 2^-24
+  float o[NT][G][4][4];            // sum p s (c - 8) 2^-24
   int end[NT][2], beg[NT][2];      // visible keys of the columns
-  float kappa = 1.0f;
+  float lift = 0.0f, lifted = 1.0f;  // log2 kappa, kappa: l, ob and o hold p kappa
   bool fresh = true, starts_item = false;
   int min_end = 0, max_beg = 0;    // keys that every row sees
 
@@ -375,13 +397,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     min_end = a.causal ? s.len - s.n + 1 : s.len;
     max_beg = a.window > 0 ? s.len - a.window : 0;
     fresh = true;
+    lift = 0.0f;
     starts_item = use.c == 0;
   };
 
   auto end_item = [&](bool whole) {
     const Seq& s = use.s;
     const int rows = s.n * a.group;
-    const float unscale = 1.0f / kappa;
     float* part = parts + (int64_t)(2 * w + (starts_item ? 1 : 0)) * part_floats(NT, D);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -395,7 +417,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         }
         const int row = nt * 8 + 2 * q4 + c;
         if (row >= rows) continue;
-        const float top = m[nt][c] * sigma[nt][c];  // log2 units; -inf: nothing seen
+        const float top = m[nt][c] * sigma[nt][c] - lift;  // log2 units; -inf: nothing seen
         const int t = s.first + row / a.group, hq = use.h * a.group + row % a.group;
         const float inv = l[nt][c] == 0.0f ? 0.0f : 1.0f / l[nt][c];
 #pragma unroll
@@ -404,7 +426,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
           // tile i, row r8 and r8 + 8: nibbles (0, 2), (1, 3), (4, 6), (5, 7)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float f = (i & 1 ? 1048576.0f : 16777216.0f) * unscale;
+            const float f = i & 1 ? 1048576.0f : 16777216.0f;
             const int ka = (i >> 1) * 4 + (i & 1);
             v[ka] = fmaf(o[nt][g][i][c], f, ob[nt][c][g]);
             v[ka + 2] = fmaf(o[nt][g][i][2 + c], f, ob[nt][c][g]);
@@ -459,184 +481,183 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     const uint32_t base = ring + stage * kStage;
     const uint32_t kc = base, vc = base + kCodes, kp = base + 2 * kCodes, vp = kp + kParams;
     const int t0 = (use.s.c0 + use.c) * kChunk;
-    const bool full = t0 >= max_beg && t0 + kChunk <= min_end;  // every row sees every key
-
-    // scores
-    float x[NT][4][4];
+    auto chunk = [&](auto all) {  // all: every row sees every key
+      constexpr bool kAll = decltype(all)::value;
+      // scores
+      float x[NT][4][4];
 #pragma unroll
-    for (int tile = 0; tile < 4; ++tile) {
-      uint32_t kw[2][2 * G], pw[2][G];
+      for (int tile = 0; tile < 4; ++tile) {
+        uint32_t kw[2][2 * G], pw[2][G];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int tok = tile * 16 + hh * 8 + kt;
-        lds(kw[hh], kc + tok * (D / 2) + q4 * (8 * G));
-        lds(pw[hh], kp + tok * (G * 4));
-      }
-      float acc[NT][G][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[nt][g][k] = 0.0f;
-#pragma unroll
-      for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const uint32_t u = kw[0][jj * G + g], v = kw[1][jj * G + g];
-          const uint32_t us = u >> 8, vs = v >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816(acc[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u, qf[nt][g][jj][0],
-                     qf[nt][g][jj][1]);
-            mma16816(acc[nt][g], us & 0x000F000Fu, vs & 0x000F000Fu, us & 0x00F000F0u, vs & 0x00F000F0u,
-                     qf[nt][g][jj][2], qf[nt][g][jj][3]);
-          }
+        for (int hh = 0; hh < 2; ++hh) {
+          const int tok = tile * 16 + hh * 8 + kt;
+          lds(kw[hh], kc + tok * (D / 2) + q4 * (8 * G));
+          lds(pw[hh], kp + tok * (G * 4));
         }
+        float acc[NT][G][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[nt][tile][k] = 0.0f;
+          for (int g = 0; g < G; ++g) {
+            const uint32_t u = kw[0][jj * G + g], v = kw[1][jj * G + g];
+            const uint32_t us = u >> 8, vs = v >> 8;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float2 so0 = half2_f32(pw[0][g]), so1 = half2_f32(pw[1][g]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (jj == 0)
+                mma16816_zero(acc[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                              qf[nt][g][jj][0], qf[nt][g][jj][1]);
+              else
+                mma16816(acc[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                         qf[nt][g][jj][0], qf[nt][g][jj][1]);
+              mma16816(acc[nt][g], us & 0x000F000Fu, vs & 0x000F000Fu, us & 0x00F000F0u, vs & 0x00F000F0u,
+                       qf[nt][g][jj][2], qf[nt][g][jj][3]);
+            }
+          }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            x[nt][tile][c] = fmaf(acc[nt][g][c], so0.x, fmaf(so0.y, qs[nt][c][g], x[nt][tile][c]));
-            x[nt][tile][2 + c] = fmaf(acc[nt][g][2 + c], so1.x, fmaf(so1.y, qs[nt][c][g], x[nt][tile][2 + c]));
-          }
-      }
-    }
-    if (!full) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int tile = 0; tile < 4; ++tile)
-#pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int t = t0 + tile * 16 + (k >> 1) * 8 + kt;
-            if (t < beg[nt][k & 1] || t >= end[nt][k & 1]) x[nt][tile][k] = -INFINITY;
+            float v = 0.0f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const float2 so = half2_f32(pw[k >> 1][g]);
+              v = g == 0 ? so.y * qs[nt][k & 1][g] : fmaf(so.y, qs[nt][k & 1][g], v);
+              v = fmaf(acc[nt][g][k], so.x, v);
+            }
+            if constexpr (!kAll) {
+              const int t = t0 + tile * 16 + (k >> 1) * 8 + kt;
+              if (t < beg[nt][k & 1] || t >= end[nt][k & 1]) v = -INFINITY;
+            }
+            x[nt][tile][k] = v;
           }
-    }
-
-    // the values' params; the largest scale among keys that any row sees
-    uint32_t vw[4][2][G];
-    uint32_t smax = 0;
-#pragma unroll
-    for (int tile = 0; tile < 4; ++tile)
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int tok = tile * 16 + hh * 8 + kt;
-        lds(vw[tile][hh], vp + tok * (G * 4));
-        const bool in = full || (t0 + tok >= use.s.lo && t0 + tok < use.s.len);
-#pragma unroll
-        for (int g = 0; g < G; ++g) smax = max(smax, in ? vw[tile][hh][g] & 0x7FFFu : 0u);
       }
-    smax = min(__reduce_max_sync(0xffffffffu, smax), 0x7BFFu);  // fp16 bits order like the values
-    const float stop = __half2float(__ushort_as_half((unsigned short)smax));
-    float drop = 1.0f;
-    if (fresh || stop * kappa > 32768.0f) {  // a first scale, or one that p s kappa would not hold in fp16
-      const int e = 8 - ((int)(__float_as_uint(stop) >> 23) - 127);
-      const float was = kappa;
-      kappa = __uint_as_float((uint32_t)(127 + min(e, 40)) << 23);
-      drop = fresh ? 0.0f : kappa / was;
-      fresh = false;
-    }
 
-    // running maximum
-    bool moved = drop != 1.0f;
-    float corr[NT][2], mneg[NT][2];
+      // the values' params; the largest scale among keys that any row sees
+      uint32_t vw[4][2][G];
+      uint32_t smax = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int tile = 0; tile < 4; ++tile)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float t = m[nt][c];
+        for (int hh = 0; hh < 2; ++hh) {
+          const int tok = tile * 16 + hh * 8 + kt;
+          lds(vw[tile][hh], vp + tok * (G * 4));
+          const bool in = kAll || (t0 + tok >= use.s.lo && t0 + tok < use.s.len);
 #pragma unroll
-        for (int tile = 0; tile < 4; ++tile) t = fmaxf(t, fmaxf(x[nt][tile][c], x[nt][tile][2 + c]));
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-        const float safe = t == -INFINITY ? 0.0f : t;
-        corr[nt][c] = ex2((m[nt][c] - safe) * sigma[nt][c]);
-        moved |= t != m[nt][c];
-        m[nt][c] = t;
-        mneg[nt][c] = -safe * sigma[nt][c];
+          for (int g = 0; g < G; ++g)
+            if (in) smax = max_halves(smax, vw[tile][hh][g]);
+        }
+      // fp16 bits order like the values (a scale is not negative)
+      smax = min(__reduce_max_sync(0xffffffffu, smax & 0x7FFFu), 0x7BFFu);
+      const float stop = __half2float(__ushort_as_half((unsigned short)smax));
+      float shift = lift;
+      if (fresh || stop * lifted > 32768.0f) {  // a first scale, or one that p s kappa would not hold in fp16
+        const int e = min(40, 8 - ((int)(__float_as_uint(stop) >> 23) - 127));
+        lifted = __uint_as_float((uint32_t)(127 + e) << 23);
+        lift = (float)e;
+        fresh = false;
       }
-    if (__any_sync(0xffffffffu, moved)) {
+      shift = lift - shift;
+
+      // running maximum
+      bool moved = shift != 0.0f;
+      float corr[NT][2], mneg[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          l[nt][c] *= corr[nt][c];
-          const float f = corr[nt][c] * drop;
+          float t = m[nt][c];
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            ob[nt][c][g] *= corr[nt][c];
+          for (int tile = 0; tile < 4; ++tile) t = fmaxf(t, fmaxf(x[nt][tile][c], x[nt][tile][2 + c]));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              o[nt][g][k][c] *= f;
-              o[nt][g][k][2 + c] *= f;
-            }
-          }
+          for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+          const float safe = t == -INFINITY ? 0.0f : t;
+          corr[nt][c] = ex2(fmaf(m[nt][c] - safe, sigma[nt][c], shift));
+          moved |= t != m[nt][c];
+          m[nt][c] = t;
+          mneg[nt][c] = fmaf(-safe, sigma[nt][c], lift);
         }
-    }
-
-    // probabilities and the second product
+      if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-    for (int tile = 0; tile < 4; ++tile) {
-      uint32_t pf[NT][G][2];
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        float2 so[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) so[g] = half2_f32(vw[tile][hh][g]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p[2];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            p[c] = ex2(fmaf(x[nt][tile][2 * hh + c], sigma[nt][c], mneg[nt][c]));
-            l[nt][c] += p[c];
+            l[nt][c] *= corr[nt][c];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              ob[nt][c][g] *= corr[nt][c];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                o[nt][g][k][c] *= corr[nt][c];
+                o[nt][g][k][2 + c] *= corr[nt][c];
+              }
+            }
           }
+      }
+
+      // probabilities (times kappa) and the second product
+#pragma unroll
+      for (int tile = 0; tile < 4; ++tile) {
+        uint32_t pf[NT][G][2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float2 so[G];
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            const float sk = so[g].x * kappa;
-            float a0 = p[0] * sk, a1 = p[1] * sk;
-            float b0 = p[0] * so[g].y, b1 = p[1] * so[g].y;
-            if (!full) {  // a hidden key's params may be anything
-              if (x[nt][tile][2 * hh] == -INFINITY) a0 = b0 = 0.0f;
-              if (x[nt][tile][2 * hh + 1] == -INFINITY) a1 = b1 = 0.0f;
-            }
-            ob[nt][0][g] += b0;
-            ob[nt][1][g] += b1;
-            pf[nt][g][hh] = transpose8x8(half2_bits(a0, a1));
+            so[g] = half2_f32(vw[tile][hh][g]);
+            so[g].y = fmaf(8.0f, so[g].x, so[g].y);
           }
-        }
-      }
-      uint32_t v0[2][G], v1[2][G];
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        lds(v0[hh], vc + (tile * 16 + hh * 8 + vt0) * (D / 2) + r8 * (4 * G));
-        lds(v1[hh], vc + (tile * 16 + hh * 8 + vt1) * (D / 2) + r8 * (4 * G));
-      }
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // nibbles 0..3, 4..7
-          const uint32_t sel = half ? 0x7632u : 0x5410u;
-          const uint32_t e = __byte_perm(v0[0][g], v1[0][g], sel), f = __byte_perm(v0[1][g], v1[1][g], sel);
-          const uint32_t es = e >> 8, fs = f >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma16816(o[nt][g][2 * half], e & 0x000F000Fu, es & 0x000F000Fu, f & 0x000F000Fu, fs & 0x000F000Fu,
-                     pf[nt][g][0], pf[nt][g][1]);
-            mma16816(o[nt][g][2 * half + 1], e & 0x00F000F0u, es & 0x00F000F0u, f & 0x00F000F0u, fs & 0x00F000F0u,
-                     pf[nt][g][0], pf[nt][g][1]);
+            float p[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              p[c] = ex2(fmaf(x[nt][tile][2 * hh + c], sigma[nt][c], mneg[nt][c]));
+              l[nt][c] += p[c];
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              float ps[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                if (kAll || x[nt][tile][2 * hh + c] != -INFINITY) {  // a hidden key's params may be anything
+                  ps[c] = p[c] * so[g].x;
+                  ob[nt][c][g] = fmaf(p[c], so[g].y, ob[nt][c][g]);
+                } else {
+                  ps[c] = 0.0f;
+                }
+              }
+              pf[nt][g][hh] = transpose8x8(half2_bits(ps[0], ps[1]));
+            }
+          }
+        }
+        uint32_t v0[2][G], v1[2][G];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          lds(v0[hh], vc + (tile * 16 + hh * 8 + vt0) * (D / 2) + r8 * (4 * G));
+          lds(v1[hh], vc + (tile * 16 + hh * 8 + vt1) * (D / 2) + r8 * (4 * G));
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // nibbles 0..3, 4..7
+            const uint32_t sel = half ? 0x7632u : 0x5410u;
+            const uint32_t e = __byte_perm(v0[0][g], v1[0][g], sel), f = __byte_perm(v0[1][g], v1[1][g], sel);
+            const uint32_t es = e >> 8, fs = f >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(o[nt][g][2 * half], e & 0x000F000Fu, es & 0x000F000Fu, f & 0x000F000Fu, fs & 0x000F000Fu,
+                       pf[nt][g][0], pf[nt][g][1]);
+              mma16816(o[nt][g][2 * half], kMinus8, kMinus8, kMinus8, kMinus8, pf[nt][g][0], pf[nt][g][1]);
+              mma16816(o[nt][g][2 * half + 1], e & 0x00F000F0u, es & 0x00F000F0u, f & 0x00F000F0u, fs & 0x00F000F0u,
+                       pf[nt][g][0], pf[nt][g][1]);
+              mma16816(o[nt][g][2 * half + 1], kMinus128, kMinus128, kMinus128, kMinus128, pf[nt][g][0], pf[nt][g][1]);
+            }
           }
         }
       }
-    }
+    };
+    if (t0 >= max_beg && t0 + kChunk <= min_end) chunk(std::true_type{});
+    else chunk(std::false_type{});
 
     // refill the stage
     __syncwarp();
