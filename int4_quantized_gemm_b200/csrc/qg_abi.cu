@@ -863,6 +863,7 @@ qg_status qg_attention_kv4(const void* q, int64_t q_stride_t, int64_t q_stride_h
   a.heads_q = (int)heads_q;
   a.group = (int)heads_q / a.cache.heads;
   a.max_pages = (int)max_pages;
+  a.page_magic = ((1ull << 40) + a.cache.page_size / 16 - 1) / (a.cache.page_size / 16);
   a.scale = scale;
   a.causal = causal != 0;
   a.window = (int)std::min<int64_t>(window, kMaxDim - 1);

@@ -123,7 +123,7 @@ static int decode_tiles(int64_t n, int64_t group, bool ragged) {
 
 size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t dim, bool ragged) {
   const int nt = decode_tiles(T / B, heads_q / heads, ragged);
-  return nt ? attention_kv4_decode_workspace(B, dim, nt) : 0;
+  return nt ? attention_kv4_decode_workspace(dim, nt) : 0;
 }
 
 qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s) {

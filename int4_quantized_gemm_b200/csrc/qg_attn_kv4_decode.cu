@@ -15,7 +15,7 @@
 // by a power of two to fp16 (1/16 of it where they meet a nibble four bits up),
 // scale and offset enter per token and group in binary32.  p s is rounded to
 // fp16 under a power of two kappa (a shift of the running maximum) that keeps
-// the largest near 2^8.  Codes are
+// s kappa near 2^4 at p = 1, 2^18 above the first fp16 subnormal.  Codes are
 // taken from their middle (a second product with the constant -8, cheaper than
 // changing the codes) because values have either sign: without it the sum over
 // n keys is large against the result and its truncation shows (0.0013 instead
@@ -23,20 +23,25 @@
 //
 // mma.m16n8k16 with keys (16 tokens) or channels (16 of V^T) as its rows and up
 // to 8 query rows as its columns: the accumulators of q.c and of the output
-// have the same columns in the same lanes, so the running maximum needs no
-// exchange, and movmatrix turns the probabilities into the second product's
-// operand.  (tcgen05 would take the codes through shared or tensor memory:
-// more bytes moved per code than this has instructions.)
+// have the same columns in the same lanes, and movmatrix turns the
+// probabilities into the second product's operand.  (tcgen05 would take the
+// codes through shared or tensor memory: more bytes moved per code than this
+// has instructions.)  The maximum that scores are taken against moves only when
+// a tile of 16 keys passes it by 8 binary digits: a vote per tile instead of a
+// reduction, and 16 keys at a time keep a warp's state small.
 //
-// Every warp is a worker of its own: the chunks of 64 tokens of all sequences
+// Every warp is a worker of its own: the chunks of tokens of all sequences
 // and heads form one list, split evenly over the warps of one CTA per SM, so
 // ragged lengths balance.  A warp streams its share through a ring of
 // bulk copies (one per page piece and array) without any block barrier.  A
-// (sequence, head) that one warp covers is written at once; the parts of one
-// that several cover are joined by a second kernel in list order (no atomics).
+// (sequence, head) that one warp covers is written at once; parts are joined
+// in list order, first those of one CTA by the CTA, then those that cross CTAs
+// by a second kernel (no atomics: the same call gives the same bits).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "qg_device.cuh"
 #include "qg_internal.h"
@@ -56,9 +61,17 @@ unsigned long long read_clear_status_attn(cudaStream_t s) {
 
 namespace {
 
-constexpr int kChunk = 64;   // tokens per ring stage
-constexpr int kWarps = 8;    // workers per CTA
-constexpr int kStages = 2;
+#ifndef V_CHUNK
+#define V_CHUNK 64
+#define V_WARPS 12
+#define V_STAGES 2
+#endif
+constexpr int kChunk = V_CHUNK;   // tokens per ring stage
+constexpr int kTiles = kChunk / 16;
+template <int NT>
+constexpr int kWarpsOf = NT == 1 ? V_WARPS : 8;  // workers per CTA (registers: 65536 / (32 workers))
+constexpr int kStages = V_STAGES;
+constexpr float kAhead = 8.0f;  // log2 of how far a score may pass the maximum it is taken against
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // fp16x2: -8 2^-24, -128 2^-24
 
 // device status sites
@@ -166,23 +179,101 @@ struct Cursor {
   }
 };
 
-// Workers share the list evenly: worker w of W has units [U w / W, U (w + 1) / W).
-__device__ __forceinline__ int64_t share(int64_t U, int64_t w, int64_t W) { return U * w / W; }
-__device__ __forceinline__ int worker_of(int64_t unit, int64_t U, int64_t W) { return (int)(((unit + 1) * W - 1) / U); }
+// The list's split: `act` warps of each CTA work, worker cta * act + warp of W
+// has units [U w / W, U (w + 1) / W).  No CTA before the last worker's is empty.
+struct Split {
+  int64_t U, W;
+  int act;
+  __device__ __forceinline__ Split(int64_t units, int grid, int warps) : U(units) {
+    act = (int)min((int64_t)warps, (U + grid - 1) / grid);
+    W = act == 1 ? min(U, (int64_t)grid) : (int64_t)grid * act;
+  }
+  __device__ __forceinline__ int first(int w) const { return (int)(U * w / W); }
+  __device__ __forceinline__ int worker_of(int64_t unit) const { return (int)(((unit + 1) * W - 1) / U); }
+};
 
-// One worker's part of a (sequence, head): rows of dim sums, then m and l.
+// A part of a (sequence, head): rows of dim sums, then (log2 of the maximum, l) of each row.
 __host__ __device__ constexpr int part_floats(int nt, int dim) { return 8 * nt * (dim + 2); }
 
+// What crosses from a CTA into the next ones: the join kernel's work.
+struct Crossing {
+  int b, h, ctas;  // ctas: how many the (sequence, head) spans from this one; 0: none
+  int pad;
+};
+
+// Parts of the two levels and the crossings, in the workspace.
+struct Scratch {
+  Crossing* crossing;  // [grid]
+  float* warp_parts;   // [grid * kWarps][2]: a continued item, an unfinished one
+  float* cta_parts;    // [grid][2]
+};
+
+// Adds `count` parts (part(i)) of `row` into v (V values per lane), returns (log2 maximum, sum).
+template <int D, int NT, class F>
+__device__ __forceinline__ float2 add_parts(F part, int count, int row, int lane, float (&v)[D / 32]) {
+  constexpr int V = D / 32;
+  float top = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) v[k] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const float* p = part(i);
+    const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * D + 2 * row);
+    float x[V];
+    if constexpr (V == 4)
+      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p + row * D + V * lane);
+    else
+      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p + row * D + V * lane);
+    const float t = fmaxf(top, ml.x), safe = t == -INFINITY ? 0.0f : t;
+    const float f = ex2(top - safe), g = ex2(ml.x - safe);
+    l = l * f + ml.y * g;
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = fmaf(x[k], g, v[k] * f);
+    top = t;
+  }
+  return make_float2(top, l);
+}
+
+// out (and lse) of one row from its sums, V values per lane
+template <int D>
+__device__ __forceinline__ void write_row(const Attn4& a, int t, int hq, int lane, const float (&v)[D / 32], float top,
+                                          float l) {
+  constexpr int V = D / 32;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t b[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const float x = l == 0.0f ? 0.0f : v[2 * i] * inv, y = l == 0.0f ? 0.0f : v[2 * i + 1] * inv;
+    if (a.dtype == QG_F16) {
+      b[i] = half2_bits(x, y);
+    } else {
+      __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      b[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+  }
+  char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+  else *reinterpret_cast<uint32_t*>(p) = b[0];
+  if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
+}
+
 template <int G, int NT>
-__global__ void __launch_bounds__(32 * kWarps, 1)
-    attention_kv4_decode(const __grid_constant__ Attn4 a, int32_t* __restrict__ prefix_out, float* __restrict__ parts) {
+__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
+    attention_kv4_decode(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch) {
+  constexpr int kWarps = kWarpsOf<NT>;
   constexpr int D = 64 * G;
   constexpr uint32_t kCodes = kChunk * D / 2, kParams = kChunk * G * 4;
   constexpr uint32_t kStage = 2 * (kCodes + kParams);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ int warp_sums[kWarps];
-  int* prefix = reinterpret_cast<int*>(smem + kWarps * kStages * kStage);
+  // a warp's parts: of an item that another worker started (1: goes on behind this worker, 2: ends here), and of
+  // one that starts here and goes on
+  struct Left {
+    int head, head_b, head_h, tail, tail_b, tail_h, tail_last;
+  };
+  __shared__ Left left[kWarps];
+  int* prefix = reinterpret_cast<int*>(smem);  // before the ring is used
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const int q4 = lane & 3, r8 = lane >> 2;
@@ -225,17 +316,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       }
     }
     __syncthreads();
-    if (blockIdx.x == 0)
-      for (int b = tid; b <= a.B; b += 32 * kWarps) prefix_out[b] = prefix[b];
   }
-  const int64_t U = prefix[a.B];
-  const int64_t W = min(U, (int64_t)gridDim.x * kWarps);
-  const int w = warp * gridDim.x + blockIdx.x;  // neighbours in the list on different SMs
-  if (w >= W) return;
-  const int u0 = (int)share(U, w, W), u1 = (int)share(U, w + 1, W);
+  const Split split(prefix[a.B], gridDim.x, kWarps);
+  const int w = blockIdx.x * split.act + warp;
+  const bool works = warp < split.act && w < split.W;
+  if (lane == 0) left[warp].head = left[warp].tail = 0;
+  const int u0 = works ? split.first(w) : 0, u1 = works ? split.first(w + 1) : 0;
 
-  Cursor<NT> fill;
-  {
+  Cursor<NT> fill = {};
+  if (u1 > u0) {
     int lo = 0, hi = a.B;  // the last b with prefix[b] <= u0 (its chunks are not 0)
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -250,6 +339,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     fill.c = in - fill.h * fill.s.chunks;
   }
   Cursor<NT> use = fill;
+  __syncthreads();  // the prefix has been read: its place is the ring's
+  fence_proxy_async_smem();
 
   // --- the ring -------------------------------------------------------------
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
@@ -268,7 +359,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     page = -1;
     const int t = (fill.s.c0 + fill.c) * kChunk + pc * piece;
     if (copies && t < fill.s.len) {
-      const int i = t / P;
+      const int i = (int)(((uint64_t)(uint32_t)(t >> 4) * a.page_magic) >> 40);  // t / P
       in_page = t - i * P;
       page = __ldg(a.table + (int64_t)fill.b * a.table_ld + i);
       if (page < 0 || page >= a.cache.pages) {
@@ -293,7 +384,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   };
 
   const int units = u1 - u0;
-  look_up();
+  if (units > 0) look_up();
 #pragma unroll 1
   for (int i = 0; i < kStages && i < units; ++i) {
     issue(i);
@@ -307,12 +398,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   uint32_t qf[NT][G][2][4];        // queries, the second operand of q . c
   float qs[NT][2][G];              // sums of the group's queries, times 2^-24: columns 2 q4, 2 q4 + 1
   float sigma[NT][2];              // scale log2(e) 2^24 over the queries' power of two
-  float m[NT][2], l[NT][2];        // running maximum (before sigma) and sum
+  float m[NT][2], l[NT][2];        // the maximum that scores are taken against (before sigma), and the sum
+  float mneg[NT][2];               // lift - m sigma; +inf: no key seen, so that the first one sets m
   float ob[NT][2][G];              // sum p o
   float o[NT][G][4][4];            // sum p s (c - 8) 2^-24
   int end[NT][2], beg[NT][2];      // visible keys of the columns
-  float lift = 0.0f, lifted = 1.0f;  // log2 kappa, kappa: l, ob and o hold p kappa
-  bool fresh = true, starts_item = false;
+  float lift = 0.0f;               // log2 kappa: l, ob and o hold p kappa
+  uint32_t limit = 0;              // largest scale (fp16 bits) that this kappa holds
+  bool starts_item = false;
   int min_end = 0, max_beg = 0;    // keys that every row sees
 
   auto begin_item = [&]() {
@@ -381,6 +474,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
           ob[nt][c][g] = 0.0f;
         }
         m[nt][c] = -INFINITY;
+        mneg[nt][c] = INFINITY;
         l[nt][c] = 0.0f;
         const int col = nt * 8 + 2 * q4 + c;
         const int pos = s.len - s.n + min(col, rows - 1) / a.group;
@@ -396,15 +490,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     }
     min_end = a.causal ? s.len - s.n + 1 : s.len;
     max_beg = a.window > 0 ? s.len - a.window : 0;
-    fresh = true;
     lift = 0.0f;
+    limit = 0;
     starts_item = use.c == 0;
   };
 
   auto end_item = [&](bool whole) {
     const Seq& s = use.s;
     const int rows = s.n * a.group;
-    float* part = parts + (int64_t)(2 * w + (starts_item ? 1 : 0)) * part_floats(NT, D);
+    float* part = scratch.warp_parts + ((int64_t)(blockIdx.x * kWarps + warp) * 2 + starts_item) * part_floats(NT, D);
+    if (!whole && lane == 0) {
+      if (starts_item)
+        left[warp].tail = 1, left[warp].tail_b = use.b, left[warp].tail_h = use.h,
+        left[warp].tail_last = u1 - 1 + s.chunks - 1 - use.c;
+      else
+        left[warp].head = use.c + 1 == s.chunks ? 2 : 1, left[warp].head_b = use.b, left[warp].head_h = use.h;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -462,7 +563,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       }
   };
 
-  begin_item();
+  if (units > 0) begin_item();
   // the token of fragment row r (0..7): pairs (0,1), (3,2), (4,5), (7,6), which spreads the value loads over the banks
   const int kt = r8 ^ ((r8 >> 1) & 1);
   const int vt0 = 2 * q4 + (q4 & 1), vt1 = vt0 ^ 1;  // rows 2 q4 and 2 q4 + 1
@@ -475,26 +576,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       // give up: let the other copies in flight land (bounded), then leave
       for (int k = 1; k < kStages && i + k < units; ++k)
         mbar_wait(smem_u32(&bars[warp][(i + k) % kStages]), (phases >> ((i + k) % kStages)) & 1, &g_status_attn, kSiteWait);
-      return;
+      break;
     }
     phases ^= 1u << stage;
     const uint32_t base = ring + stage * kStage;
     const uint32_t kc = base, vc = base + kCodes, kp = base + 2 * kCodes, vp = kp + kParams;
     const int t0 = (use.s.c0 + use.c) * kChunk;
-    auto chunk = [&](auto all) {  // all: every row sees every key
+    auto tiles = [&](auto all) {  // all: every row sees every key
       constexpr bool kAll = decltype(all)::value;
-      // scores
-      float x[NT][4][4];
-#pragma unroll
-      for (int tile = 0; tile < 4; ++tile) {
-        uint32_t kw[2][2 * G], pw[2][G];
+#pragma unroll 2
+      for (int tile = 0; tile < kTiles; ++tile) {
+        // scores
+        uint32_t kw[2][2 * G], pw[2][G], vw[2][G];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const int tok = tile * 16 + hh * 8 + kt;
           lds(kw[hh], kc + tok * (D / 2) + q4 * (8 * G));
           lds(pw[hh], kp + tok * (G * 4));
+          lds(vw[hh], vp + tok * (G * 4));
         }
-        float acc[NT][G][4];
+        float x[NT][G][4];
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
@@ -504,106 +605,99 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               if (jj == 0)
-                mma16816_zero(acc[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                mma16816_zero(x[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
                               qf[nt][g][jj][0], qf[nt][g][jj][1]);
               else
-                mma16816(acc[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                mma16816(x[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
                          qf[nt][g][jj][0], qf[nt][g][jj][1]);
-              mma16816(acc[nt][g], us & 0x000F000Fu, vs & 0x000F000Fu, us & 0x00F000F0u, vs & 0x00F000F0u,
+              mma16816(x[nt][g], us & 0x000F000Fu, vs & 0x000F000Fu, us & 0x00F000F0u, vs & 0x00F000F0u,
                        qf[nt][g][jj][2], qf[nt][g][jj][3]);
             }
           }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int k = 0; k < 4; ++k) {
+          float2 so[G];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v = 0.0f;
+          for (int g = 0; g < G; ++g) so[g] = half2_f32(pw[k >> 1][g]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float v = so[0].y * qs[nt][k & 1][0];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              const float2 so = half2_f32(pw[k >> 1][g]);
-              v = g == 0 ? so.y * qs[nt][k & 1][g] : fmaf(so.y, qs[nt][k & 1][g], v);
-              v = fmaf(acc[nt][g][k], so.x, v);
+              if (g > 0) v = fmaf(so[g].y, qs[nt][k & 1][g], v);
+              v = fmaf(x[nt][g][k], so[g].x, v);
             }
             if constexpr (!kAll) {
               const int t = t0 + tile * 16 + (k >> 1) * 8 + kt;
               if (t < beg[nt][k & 1] || t >= end[nt][k & 1]) v = -INFINITY;
             }
-            x[nt][tile][k] = v;
+            x[nt][0][k] = v;
           }
-      }
+        }
 
-      // the values' params; the largest scale among keys that any row sees
-      uint32_t vw[4][2][G];
-      uint32_t smax = 0;
-#pragma unroll
-      for (int tile = 0; tile < 4; ++tile)
+        // does a score pass the maximum too far, or a scale (of a key that any row sees) what kappa holds?
+        uint32_t smax = 0;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const int tok = tile * 16 + hh * 8 + kt;
-          lds(vw[tile][hh], vp + tok * (G * 4));
-          const bool in = kAll || (t0 + tok >= use.s.lo && t0 + tok < use.s.len);
+          const int t = t0 + tile * 16 + hh * 8 + kt;
+          if (kAll || (t >= use.s.lo && t < use.s.len)) {
 #pragma unroll
-          for (int g = 0; g < G; ++g)
-            if (in) smax = max_halves(smax, vw[tile][hh][g]);
+            for (int g = 0; g < G; ++g) smax = max_halves(smax, vw[hh][g]);
+          }
         }
-      // fp16 bits order like the values (a scale is not negative)
-      smax = min(__reduce_max_sync(0xffffffffu, smax & 0x7FFFu), 0x7BFFu);
-      const float stop = __half2float(__ushort_as_half((unsigned short)smax));
-      float shift = lift;
-      if (fresh || stop * lifted > 32768.0f) {  // a first scale, or one that p s kappa would not hold in fp16
-        const int e = min(40, 8 - ((int)(__float_as_uint(stop) >> 23) - 127));
-        lifted = __uint_as_float((uint32_t)(127 + e) << 23);
-        lift = (float)e;
-        fresh = false;
-      }
-      shift = lift - shift;
-
-      // running maximum
-      bool moved = shift != 0.0f;
-      float corr[NT][2], mneg[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float t = m[nt][c];
-#pragma unroll
-          for (int tile = 0; tile < 4; ++tile) t = fmaxf(t, fmaxf(x[nt][tile][c], x[nt][tile][2 + c]));
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-          const float safe = t == -INFINITY ? 0.0f : t;
-          corr[nt][c] = ex2(fmaf(m[nt][c] - safe, sigma[nt][c], shift));
-          moved |= t != m[nt][c];
-          m[nt][c] = t;
-          mneg[nt][c] = fmaf(-safe, sigma[nt][c], lift);
-        }
-      if (__any_sync(0xffffffffu, moved)) {
+        smax &= 0x7FFFu;  // fp16 bits order like the values (a scale is not negative)
+        float e[NT][4], far = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            l[nt][c] *= corr[nt][c];
+          for (int k = 0; k < 4; ++k) {
+            e[nt][k] = kAll || x[nt][0][k] != -INFINITY ? fmaf(x[nt][0][k], sigma[nt][k & 1], mneg[nt][k & 1]) : -INFINITY;
+            far = fmaxf(far, e[nt][k]);
+          }
+        if (__any_sync(0xffffffffu, far > lift + kAhead || smax > limit)) {
+          smax = min(__reduce_max_sync(0xffffffffu, smax), 0x7BFFu);
+          float shift = lift;
+          if (smax > limit) {  // scale times kappa in [2^3, 2^4), up to 2^6 before this is done again; p up to 2^8
+            const uint32_t ex = max(smax >> 10, 1u);  // the scale's exponent, 15 for 1
+            lift = 18.0f - (float)ex;
+            limit = min((ex + 3) << 10, 0x7BFFu);
+          }
+          shift = lift - shift;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-              ob[nt][c][g] *= corr[nt][c];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                o[nt][g][k][c] *= corr[nt][c];
-                o[nt][g][k][2 + c] *= corr[nt][c];
+            for (int c = 0; c < 2; ++c) {
+              float t = fmaxf(m[nt][c], fmaxf(x[nt][0][c], x[nt][0][2 + c]));
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+              const float safe = t == -INFINITY ? 0.0f : t;
+              const float corr = ex2(fmaf(m[nt][c] - safe, sigma[nt][c], shift));
+              m[nt][c] = t;
+              const float mn = fmaf(-safe, sigma[nt][c], lift);
+              mneg[nt][c] = t == -INFINITY ? INFINITY : mn;
+#pragma unroll
+              for (int k = c; k < 4; k += 2) e[nt][k] = fmaf(x[nt][0][k], sigma[nt][c], mn);
+              l[nt][c] *= corr;
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+                ob[nt][c][g] *= corr;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  o[nt][g][k][c] *= corr;
+                  o[nt][g][k][2 + c] *= corr;
+                }
               }
             }
-          }
-      }
+        }
 
-      // probabilities (times kappa) and the second product
-#pragma unroll
-      for (int tile = 0; tile < 4; ++tile) {
+        // probabilities (times kappa) and the second product
         uint32_t pf[NT][G][2];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           float2 so[G];
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            so[g] = half2_f32(vw[tile][hh][g]);
+            so[g] = half2_f32(vw[hh][g]);
             so[g].y = fmaf(8.0f, so[g].x, so[g].y);
           }
 #pragma unroll
@@ -611,7 +705,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             float p[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              p[c] = ex2(fmaf(x[nt][tile][2 * hh + c], sigma[nt][c], mneg[nt][c]));
+              p[c] = ex2(e[nt][2 * hh + c]);
               l[nt][c] += p[c];
             }
 #pragma unroll
@@ -619,7 +713,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
               float ps[2];
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                if (kAll || x[nt][tile][2 * hh + c] != -INFINITY) {  // a hidden key's params may be anything
+                if (kAll || x[nt][0][2 * hh + c] != -INFINITY) {  // a hidden key's params may be anything
                   ps[c] = p[c] * so[g].x;
                   ob[nt][c][g] = fmaf(p[c], so[g].y, ob[nt][c][g]);
                 } else {
@@ -641,14 +735,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // nibbles 0..3, 4..7
             const uint32_t sel = half ? 0x7632u : 0x5410u;
-            const uint32_t e = __byte_perm(v0[0][g], v1[0][g], sel), f = __byte_perm(v0[1][g], v1[1][g], sel);
-            const uint32_t es = e >> 8, fs = f >> 8;
+            const uint32_t e0 = __byte_perm(v0[0][g], v1[0][g], sel), e1 = __byte_perm(v0[1][g], v1[1][g], sel);
+            const uint32_t f0 = e0 >> 8, f1 = e1 >> 8;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816(o[nt][g][2 * half], e & 0x000F000Fu, es & 0x000F000Fu, f & 0x000F000Fu, fs & 0x000F000Fu,
+              mma16816(o[nt][g][2 * half], e0 & 0x000F000Fu, f0 & 0x000F000Fu, e1 & 0x000F000Fu, f1 & 0x000F000Fu,
                        pf[nt][g][0], pf[nt][g][1]);
               mma16816(o[nt][g][2 * half], kMinus8, kMinus8, kMinus8, kMinus8, pf[nt][g][0], pf[nt][g][1]);
-              mma16816(o[nt][g][2 * half + 1], e & 0x00F000F0u, es & 0x00F000F0u, f & 0x00F000F0u, fs & 0x00F000F0u,
+              mma16816(o[nt][g][2 * half + 1], e0 & 0x00F000F0u, f0 & 0x00F000F0u, e1 & 0x00F000F0u, f1 & 0x00F000F0u,
                        pf[nt][g][0], pf[nt][g][1]);
               mma16816(o[nt][g][2 * half + 1], kMinus128, kMinus128, kMinus128, kMinus128, pf[nt][g][0], pf[nt][g][1]);
             }
@@ -656,8 +750,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         }
       }
     };
-    if (t0 >= max_beg && t0 + kChunk <= min_end) chunk(std::true_type{});
-    else chunk(std::false_type{});
+    if (t0 >= max_beg && t0 + kChunk <= min_end) tiles(std::true_type{});
+    else tiles(std::false_type{});
 
     // refill the stage
     __syncwarp();
@@ -676,105 +770,139 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
       if (item_done) begin_item();
     }
   }
+  // --- what the warps left unfinished -----------------------------------------
+  // In list order: each warp's continued item, then the one it started.  A group of parts that belong together
+  // begins with a started item (or the CTA's first part) and takes every continued one up to the item's end.
+  __syncthreads();
+  const float* base = scratch.warp_parts + (int64_t)blockIdx.x * kWarps * 2 * part_floats(NT, D);
+  int groups = 0;
+  Crossing cross = {0, 0, 0, 0};
+  for (int i = 0; i < 2 * split.act;) {
+    const int kind = i & 1 ? left[i / 2].tail : left[i / 2].head;
+    if (kind == 0) {
+      ++i;
+      continue;
+    }
+    const bool starts = i & 1;
+    const int b = starts ? left[i / 2].tail_b : left[i / 2].head_b, h = starts ? left[i / 2].tail_h : left[i / 2].head_h;
+    const int from = i;
+    bool ends = !starts && kind == 2;
+    int count = 1, last = i;  // parts at from, then heads (even places) up to last
+    for (i = (i | 1) + 1; !ends && i < 2 * split.act; i += 2) {
+      if (left[i / 2].head == 0) {
+        if (left[i / 2].tail) break;  // cannot be: an item in progress is continued first
+        continue;                     // a worker without units
+      }
+      ++count;
+      last = i;
+      ends = left[i / 2].head == 2;
+    }
+    // the search goes on behind the last head taken: its own warp may have started another item
+    i = last + 1;
+    if (starts && !ends) cross = {b, h, split.worker_of(left[from / 2].tail_last) / split.act - (int)blockIdx.x + 1, 0};
+    int first, n, len;
+    attn4_sequence(a, b, first, n, len);
+    float* to = scratch.cta_parts + (int64_t)(blockIdx.x * 2 + starts) * part_floats(NT, D);
+    for (int row = (warp + groups) % kWarps; row < n * a.group; row += kWarps) {
+      float v[D / 32];
+      int place = from;
+      const float2 tl = add_parts<D, NT>(
+          [&](int k) -> const float* {  // called in order: the heads behind `from` that hold a part
+            if (k > 0)
+              do place = (place | 1) + 1;
+              while (left[place / 2].head == 0);
+            return base + (int64_t)place * part_floats(NT, D);
+          },
+          count, row, lane, v);
+      if (starts && ends) {
+        write_row<D>(a, first + row / a.group, h * a.group + row % a.group, lane, v, tl.x, tl.y);
+      } else {
+        if constexpr (G == 2) *reinterpret_cast<float4*>(to + row * D + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<float2*>(to + row * D + 2 * lane) = make_float2(v[0], v[1]);
+        if (lane == 0) *reinterpret_cast<float2*>(to + 8 * NT * D + 2 * row) = tl;
+      }
+    }
+    ++groups;
+  }
+  if (tid == 0) scratch.crossing[blockIdx.x] = cross;
 }
 
-// Joins the parts of the (sequence, head)s that several workers share: block
-// (row, head, sequence), a warp per part in turn, the sums over warps in order.
-template <int D>
+// Joins the parts of the (sequence, head)s that cross CTAs: block (row, CTA in which it starts), the CTAs' parts
+// in eight strands that are then added in order.
+template <int D, int NT>
 __global__ void __launch_bounds__(256)
-    attention_kv4_join(const __grid_constant__ Attn4 a, const int32_t* __restrict__ prefix,
-                       const float* __restrict__ parts, int workers, int nt) {
-  constexpr int V = D / 32;  // values per lane
-  __shared__ float sums[8][D];
-  __shared__ float ls[8];
+    attention_kv4_join(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch) {
+  constexpr int V = D / 32;
+  __shared__ __align__(16) float sums[8][D];
+  __shared__ float2 tls[8];
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int i0 = prefix[b], i1 = prefix[b + 1];
-  if (i1 == i0) return;
+  const int row = blockIdx.x, cta = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const Crossing c = scratch.crossing[cta];
+  if (c.ctas == 0) return;
   int first, n, len;
-  attn4_sequence(a, b, first, n, len);
+  attn4_sequence(a, c.b, first, n, len);
   if (row >= n * a.group) return;
-  const int64_t U = prefix[a.B], W = min(U, (int64_t)workers);
-  const int chunks = (i1 - i0) / a.cache.heads;
-  const int64_t u = i0 + (int64_t)h * chunks;
-  const int wa = worker_of(u, U, W), wb = worker_of(u + chunks - 1, U, W);
-  if (wa == wb) return;
-  const int rows = 8 * nt, stride = rows * (D + 2), count = wb - wa + 1;
-  auto part = [&](int i) { return parts + (int64_t)(2 * (wa + i) + (i == 0 ? 1 : 0)) * stride; };
-
-  float top = -INFINITY;
-  for (int i = lane; i < count; i += 32) top = fmaxf(top, part(i)[rows * D + 2 * row]);
+  const int each = (c.ctas + 7) / 8, from = warp * each;
+  float v[V];
+  float2 tl = add_parts<D, NT>(
+      [&](int i) -> const float* {
+        const int k = from + i;
+        return scratch.cta_parts + (int64_t)((cta + k) * 2 + (k == 0)) * part_floats(NT, D);
+      },
+      max(0, min(each, c.ctas - from)), row, lane, v);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float safe = top == -INFINITY ? 0.0f : top;
-  float acc[V] = {}, l = 0.0f;
-#pragma unroll 4
-  for (int i = warp; i < count; i += 8) {
-    const float* p = part(i);
-    const float2 ml = *reinterpret_cast<const float2*>(p + rows * D + 2 * row);
-    const float f = ex2(ml.x - safe);
-    l += ml.y * f;
-    float v[V];
-    if constexpr (V == 4)
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p + row * D + V * lane);
-    else
-      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p + row * D + V * lane);
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = fmaf(v[k], f, acc[k]);
-  }
-#pragma unroll
-  for (int k = 0; k < V; ++k) sums[warp][V * lane + k] = acc[k];
-  if (lane == 0) ls[warp] = l;
+  for (int k = 0; k < V; ++k) sums[warp][V * lane + k] = v[k];
+  if (lane == 0) tls[warp] = tl;
   __syncthreads();
-  float total = 0.0f;
+  if (warp != 0) return;
+  float top = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) total += ls[w];
-  const int t = first + row / a.group, hq = h * a.group + row % a.group;
-  if (threadIdx.x < D) {
-    float v = 0.0f;
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, tls[i].x);
+  const float safe = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += sums[w][threadIdx.x];
-    v = total == 0.0f ? 0.0f : v / total;
-    const int64_t at = t * a.o_st + hq * a.o_sh + threadIdx.x;
-    if (a.dtype == QG_F16) static_cast<__half*>(a.out)[at] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+  for (int k = 0; k < V; ++k) v[k] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f = ex2(tls[i].x - safe);
+    l = fmaf(tls[i].y, f, l);
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = fmaf(sums[i][V * lane + k], f, v[k]);
   }
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(int64_t)t * a.heads_q + hq] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.69314718056f;
+  write_row<D>(a, first + row / a.group, c.h * a.group + row % a.group, lane, v, top, l);
 }
 
-size_t prefix_bytes(int64_t B) { return (size_t)((B + 1) * 4 + 15) / 16 * 16; }
+size_t crossing_bytes() { return (size_t)sm_count() * sizeof(Crossing); }
 
 template <int G, int NT>
 qg_status launch(const Attn4& a, void* workspace, cudaStream_t s) {
-  constexpr int D = 64 * G;
+  constexpr int D = 64 * G, kWarps = kWarpsOf<NT>;
   constexpr int kRing = kWarps * kStages * 2 * kChunk * (D / 2 + 4 * G);
+  constexpr int kMost = kRing > 4097 * 4 ? kRing : 4097 * 4;  // the prefix of 4096 sequences shares the ring's place
   static PerDeviceOnce once;
   const qg_status st = once.run([](int) {
-    return check_cuda(cudaFuncSetAttribute(attention_kv4_decode<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kRing + (4096 + 1) * 4),
+    return check_cuda(cudaFuncSetAttribute(attention_kv4_decode<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost),
                       "attention_kv4 shared memory");
   });
   if (st != QG_OK) return st;
-  int32_t* prefix = static_cast<int32_t*>(workspace);
-  float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(a.B));
   const int grid = sm_count();
-  LaunchCfg lc((unsigned)grid, 32 * kWarps, kRing + (a.B + 1) * 4, s);
-  cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_decode<G, NT>, a, prefix, parts);
+  Scratch scratch;
+  scratch.crossing = static_cast<Crossing*>(workspace);
+  scratch.warp_parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + crossing_bytes());
+  scratch.cta_parts = scratch.warp_parts + (int64_t)grid * kWarps * 2 * part_floats(NT, D);
+  LaunchCfg lc((unsigned)grid, 32 * kWarps, kMost, s);
+  cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_decode<G, NT>, a, scratch);
   if (e != cudaSuccess) return check_cuda(e, "attention_kv4 decode launch");
-  LaunchCfg lj(8 * NT, 256, 0, s);
-  lj.cfg.gridDim.y = (unsigned)a.cache.heads;
-  lj.cfg.gridDim.z = (unsigned)a.B;
-  e = cudaLaunchKernelEx(&lj.cfg, attention_kv4_join<D>, a, (const int32_t*)prefix, (const float*)parts, grid * kWarps, NT);
+  LaunchCfg lj((unsigned)std::min(8 * NT, a.q_starts ? 8 * NT : a.n_uniform * a.group), 256, 0, s);
+  lj.cfg.gridDim.y = (unsigned)grid;
+  e = cudaLaunchKernelEx(&lj.cfg, attention_kv4_join<D, NT>, a, scratch);
   return check_cuda(e, "attention_kv4 join launch");
 }
 
 }  // namespace
 
-size_t attention_kv4_decode_workspace(int64_t B, int64_t dim, int nt) {
-  return prefix_bytes(B) + (size_t)2 * sm_count() * kWarps * part_floats(nt, (int)dim) * sizeof(float);
+size_t attention_kv4_decode_workspace(int64_t dim, int nt) {
+  return crossing_bytes() + (size_t)sm_count() * ((nt == 1 ? kWarpsOf<1> : kWarpsOf<2>) + 1) * 2 * part_floats(nt, (int)dim) * sizeof(float);
 }
 
 qg_status launch_attention_kv4_decode(const Attn4& a, int nt, void* workspace, cudaStream_t s) {

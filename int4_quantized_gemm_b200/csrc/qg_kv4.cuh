@@ -46,6 +46,7 @@ struct Attn4 {
   int n_uniform;
   int B, T, heads_q, group;  // group = heads_q / heads
   int max_pages;
+  uint64_t page_magic;  // (t >> 4) * page_magic >> 40 = t / page_size for t < 2^31 (page_size / 16 <= 4096)
   float scale;
   int causal;
   int window;  // 0: none
