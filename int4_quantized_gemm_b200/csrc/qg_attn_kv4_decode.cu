@@ -7,7 +7,7 @@
 // decides the time is therefore the instructions per code, and the codes are
 // never dequantized one by one:
 //   score_j = sum_g [ s_jg (q_g . c_jg) + o_jg sum(q_g) ]
-//   out     = sum_j p_j (s_jg c_j + o_jg) = sum_j (p_j s_jg) (c_j - 8) + sum_j p_j (o_jg + 8 s_jg)
+//   out     = sum_j (p_j s_jg) (c_j - 8) + sum_j p_j (o_jg + 8 s_jg)
 // (g: group of 64 channels; s, o: its scale and offset; c: codes).  The products
 // run on the codes themselves.  A nibble masked into the low bits of a half is
 // the fp16 subnormal c 2^-24 (or, four bits up, 16 c 2^-24), exact on the tensor
@@ -27,8 +27,8 @@
 // probabilities into the second product's operand.  (tcgen05 would take the
 // codes through shared or tensor memory: more bytes moved per code than this
 // has instructions.)  The maximum that scores are taken against moves only when
-// a tile of 16 keys passes it by 8 binary digits: a vote per tile instead of a
-// reduction, and 16 keys at a time keep a warp's state small.
+// 32 keys pass it by 8 binary digits: a vote instead of a reduction, and 32 keys
+// at a time keep a warp's state small.
 //
 // Every warp is a worker of its own: the chunks of tokens of all sequences
 // and heads form one list, split evenly over the warps of one CTA per SM, so
@@ -61,16 +61,12 @@ unsigned long long read_clear_status_attn(cudaStream_t s) {
 
 namespace {
 
-#ifndef V_CHUNK
-#define V_CHUNK 64
-#define V_WARPS 12
-#define V_STAGES 2
-#endif
-constexpr int kChunk = V_CHUNK;   // tokens per ring stage
-constexpr int kTiles = kChunk / 16;
+// The ring: 64 tokens a stage and 2 stages for each of 12 warps (221 KB at 128 channels, the registers' 168 a thread).
+// 64 sequences of 4096..8192 tokens, 64/8 heads: 125 us; 8 or 10 warps 138, 147; stages of 32 tokens 141.
+constexpr int kChunk = 64;   // tokens per ring stage
 template <int NT>
-constexpr int kWarpsOf = NT == 1 ? V_WARPS : 8;  // workers per CTA (registers: 65536 / (32 workers))
-constexpr int kStages = V_STAGES;
+constexpr int kWarpsOf = NT == 1 ? 12 : 8;  // workers per CTA (registers: 65536 / (32 workers))
+constexpr int kStages = 2;
 constexpr float kAhead = 8.0f;  // log2 of how far a score may pass the maximum it is taken against
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // fp16x2: -8 2^-24, -128 2^-24
 
@@ -90,7 +86,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -99,7 +95,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // The same with a zero accumulator.
 __device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
@@ -114,7 +110,7 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -135,14 +131,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 template <int N>
-__device__ __forceinline__ void lds(uint32_t (&r)[N], uint32_t addr) {
+__device__ __forceinline__ void lds(uint32_t (&r)[N], const uint8_t* p) {
   static_assert(N == 1 || N == 2 || N == 4, "");
-  if constexpr (N == 1)
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
-  else
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+  if constexpr (N == 1) {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x, r[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  }
 }
 
 // What a sequence asks of this kernel: its chunks [c0, c0 + chunks) per head.
@@ -179,17 +178,14 @@ struct Cursor {
   }
 };
 
-// The list's split: `act` warps of each CTA work, worker cta * act + warp of W
-// has units [U w / W, U (w + 1) / W).  No CTA before the last worker's is empty.
-struct Split {
-  int64_t U, W;
-  int act;
-  __device__ __forceinline__ Split(int64_t units, int grid, int warps) : U(units) {
-    act = (int)min((int64_t)warps, (U + grid - 1) / grid);
-    W = act == 1 ? min(U, (int64_t)grid) : (int64_t)grid * act;
+// n units over `over` takers, the first n % over of them one more.
+struct Share {
+  uint32_t q, r;
+  __device__ __forceinline__ Share(uint32_t n, uint32_t over) : q(n / over), r(n - n / over * over) {}
+  __device__ __forceinline__ uint32_t first(uint32_t i) const { return q * i + min(i, r); }
+  __device__ __forceinline__ uint32_t taker(uint32_t unit) const {
+    return unit < (q + 1) * r ? unit / (q + 1) : r + (unit - (q + 1) * r) / q;
   }
-  __device__ __forceinline__ int first(int w) const { return (int)(U * w / W); }
-  __device__ __forceinline__ int worker_of(int64_t unit) const { return (int)(((unit + 1) * W - 1) / U); }
 };
 
 // A part of a (sequence, head): rows of dim sums, then (log2 of the maximum, l) of each row.
@@ -208,53 +204,84 @@ struct Scratch {
   float* cta_parts;    // [grid][2]
 };
 
-// Adds `count` parts (part(i)) of `row` into v (V values per lane), returns (log2 maximum, sum).
+// Adds `count` parts (part(i), called for i = 0, 1, ...) of the 8 rows from `row0` on.  Lane r < 8 holds the log2
+// maximum and the sum of row row0 + r; every lane V values of each row.
 template <int D, int NT, class F>
-__device__ __forceinline__ float2 add_parts(F part, int count, int row, int lane, float (&v)[D / 32]) {
+__device__ __forceinline__ void add_parts(F part, int count, int row0, int lane, float& top, float& l,
+                                          float (&v)[8][D / 32]) {
   constexpr int V = D / 32;
-  float top = -INFINITY, l = 0.0f;
+  top = -INFINITY;
+  l = 0.0f;
 #pragma unroll
-  for (int k = 0; k < V; ++k) v[k] = 0.0f;
-#pragma unroll 4
+  for (int r = 0; r < 8; ++r)
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[r][k] = 0.0f;
+#pragma unroll 1
   for (int i = 0; i < count; ++i) {
     const float* p = part(i);
-    const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * D + 2 * row);
-    float x[V];
-    if constexpr (V == 4)
-      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p + row * D + V * lane);
-    else
-      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p + row * D + V * lane);
+    const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * D + 2 * (row0 + (lane & 7)));
+    float x[8][V];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(x[r]) = *reinterpret_cast<const float4*>(p + (row0 + r) * D + V * lane);
+      else
+        *reinterpret_cast<float2*>(x[r]) = *reinterpret_cast<const float2*>(p + (row0 + r) * D + V * lane);
+    }
     const float t = fmaxf(top, ml.x), safe = t == -INFINITY ? 0.0f : t;
     const float f = ex2(top - safe), g = ex2(ml.x - safe);
     l = l * f + ml.y * g;
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = fmaf(x[k], g, v[k] * f);
     top = t;
-  }
-  return make_float2(top, l);
-}
-
-// out (and lse) of one row from its sums, V values per lane
-template <int D>
-__device__ __forceinline__ void write_row(const Attn4& a, int t, int hq, int lane, const float (&v)[D / 32], float top,
-                                          float l) {
-  constexpr int V = D / 32;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint32_t b[V / 2];
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    const float x = l == 0.0f ? 0.0f : v[2 * i] * inv, y = l == 0.0f ? 0.0f : v[2 * i + 1] * inv;
-    if (a.dtype == QG_F16) {
-      b[i] = half2_bits(x, y);
-    } else {
-      __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-      b[i] = *reinterpret_cast<uint32_t*>(&h);
+    for (int r = 0; r < 8; ++r) {
+      const float fr = __shfl_sync(0xffffffffu, f, r), gr = __shfl_sync(0xffffffffu, g, r);
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[r][k] = fmaf(x[r][k], gr, v[r][k] * fr);
     }
   }
-  char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
-  if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
-  else *reinterpret_cast<uint32_t*>(p) = b[0];
-  if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
+}
+
+// out (and lse) of the rows [row0, rows) of an item from their sums
+template <int D>
+__device__ __forceinline__ void write_rows(const Attn4& a, int first, int h, int row0, int rows, int lane, float top,
+                                           float l, const float (&v)[8][D / 32]) {
+  constexpr int V = D / 32;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const float lr = __shfl_sync(0xffffffffu, l, r), ir = __shfl_sync(0xffffffffu, inv, r);
+    const int row = row0 + r;
+    if (row < rows) {
+      const int t = first + row / a.group, hq = h * a.group + row % a.group;
+      uint32_t b[V / 2];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const float x = lr == 0.0f ? 0.0f : v[r][2 * i] * ir, y = lr == 0.0f ? 0.0f : v[r][2 * i + 1] * ir;
+        if (a.dtype == QG_F16) {
+          b[i] = half2_bits(x, y);
+        } else {
+          __nv_bfloat162 hv = __floats2bfloat162_rn(x, y);
+          b[i] = *reinterpret_cast<uint32_t*>(&hv);
+        }
+      }
+      char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+      else *reinterpret_cast<uint32_t*>(p) = b[0];
+      if (a.lse && lane == r) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
+    }
+  }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void write_part(float* p, int row0, int lane, float top, float l, const float (&v)[8][D / 32]) {
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    if constexpr (D == 128)
+      *reinterpret_cast<float4*>(p + (row0 + r) * D + 4 * lane) = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+    else
+      *reinterpret_cast<float2*>(p + (row0 + r) * D + 2 * lane) = make_float2(v[r][0], v[r][1]);
+  }
+  if (lane < 8) *reinterpret_cast<float2*>(p + 8 * NT * D + 2 * (row0 + lane)) = make_float2(top, l);
 }
 
 template <int G, int NT>
@@ -286,16 +313,16 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
   pdl_wait();
 
   // prefix[b]: chunks (times heads) of the sequences before b
+  const int per = (a.B + 32 * kWarps - 1) / (32 * kWarps);
   {
-    const int per = (a.B + 32 * kWarps - 1) / (32 * kWarps);
     int sum = 0;
-    bool ok;
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      if (b < a.B) {
-        sum += sequence<NT>(a, b, ok).chunks * a.cache.heads;
-        if (!ok && blockIdx.x == 0) report(kDevBadArg, kSiteSequence);
-      }
+#pragma unroll 1
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+      bool ok;
+      const int units = sequence<NT>(a, b, ok).chunks * a.cache.heads;
+      if (!ok && blockIdx.x == 0) report(kDevBadArg, kSiteSequence);
+      prefix[b] = units;
+      sum += units;
     }
     int scan = sum;
 #pragma unroll
@@ -307,24 +334,25 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
     __syncthreads();
     int at = scan - sum;
     for (int w = 0; w < warp; ++w) at += warp_sums[w];
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      if (b < a.B) {
-        prefix[b] = at;
-        at += sequence<NT>(a, b, ok).chunks * a.cache.heads;
-        if (b == a.B - 1) prefix[a.B] = at;
-      }
+#pragma unroll 1
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+      const int units = prefix[b];
+      prefix[b] = at;
+      at += units;
+      if (b == a.B - 1) prefix[a.B] = at;
     }
     __syncthreads();
   }
-  const Split split(prefix[a.B], gridDim.x, kWarps);
-  const int w = blockIdx.x * split.act + warp;
-  const bool works = warp < split.act && w < split.W;
+  // the list's units over the CTAs, a CTA's over its warps
+  const Share ctas((uint32_t)prefix[a.B], gridDim.x);
+  const uint32_t cta0 = ctas.first(blockIdx.x);
+  const Share warps(ctas.first(blockIdx.x + 1) - cta0, kWarps);
+  const int u0 = (int)(cta0 + warps.first(warp)), units = (int)(warps.first(warp + 1) - warps.first(warp));
+  const bool alone = warps.q == 0 && warps.r == 1;  // the CTA's one worker: its parts are the CTA's
   if (lane == 0) left[warp].head = left[warp].tail = 0;
-  const int u0 = works ? split.first(w) : 0, u1 = works ? split.first(w + 1) : 0;
 
   Cursor<NT> fill = {};
-  if (u1 > u0) {
+  if (units > 0) {
     int lo = 0, hi = a.B;  // the last b with prefix[b] <= u0 (its chunks are not 0)
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -382,17 +410,6 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
       bulk_load(ring + stage * kStage + dst_off, src, bytes, bar);
     }
   };
-
-  const int units = u1 - u0;
-  if (units > 0) look_up();
-#pragma unroll 1
-  for (int i = 0; i < kStages && i < units; ++i) {
-    issue(i);
-    if (i + 1 < units) {
-      fill.next(a);
-      look_up();
-    }
-  }
 
   // --- the item in hand -------------------------------------------------------
   uint32_t qf[NT][G][2][4];        // queries, the second operand of q . c
@@ -498,11 +515,12 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
   auto end_item = [&](bool whole) {
     const Seq& s = use.s;
     const int rows = s.n * a.group;
-    float* part = scratch.warp_parts + ((int64_t)(blockIdx.x * kWarps + warp) * 2 + starts_item) * part_floats(NT, D);
+    float* part = alone ? scratch.cta_parts + (int64_t)(blockIdx.x * 2 + starts_item) * part_floats(NT, D)
+                        : scratch.warp_parts + ((int64_t)(blockIdx.x * kWarps + warp) * 2 + starts_item) * part_floats(NT, D);
     if (!whole && lane == 0) {
       if (starts_item)
         left[warp].tail = 1, left[warp].tail_b = use.b, left[warp].tail_h = use.h,
-        left[warp].tail_last = u1 - 1 + s.chunks - 1 - use.c;
+        left[warp].tail_last = u0 + units - 1 + s.chunks - 1 - use.c;
       else
         left[warp].head = use.c + 1 == s.chunks ? 2 : 1, left[warp].head_b = use.b, left[warp].head_h = use.h;
     }
@@ -563,97 +581,118 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
       }
   };
 
-  if (units > 0) begin_item();
   // the token of fragment row r (0..7): pairs (0,1), (3,2), (4,5), (7,6), which spreads the value loads over the banks
   const int kt = r8 ^ ((r8 >> 1) & 1);
   const int vt0 = 2 * q4 + (q4 & 1), vt1 = vt0 ^ 1;  // rows 2 q4 and 2 q4 + 1
   uint32_t phases = 0;
 
+  int filled = 0;          // chunks whose copies were issued
+  bool new_item = true;
+  if (units > 0) look_up();
 #pragma unroll 1
   for (int i = 0; i < units; ++i) {
     const int stage = i % kStages;
+#pragma unroll 1
+    while (filled < units && filled < i + kStages) {  // stage (i - 1) % kStages has been read by the whole warp
+      issue(filled % kStages);
+      if (++filled < units) {
+        fill.next(a);
+        look_up();
+      }
+    }
+    if (new_item) begin_item();
     if (!mbar_wait(smem_u32(&bars[warp][stage]), (phases >> stage) & 1, &g_status_attn, kSiteWait)) {
       // give up: let the other copies in flight land (bounded), then leave
-      for (int k = 1; k < kStages && i + k < units; ++k)
+      for (int k = 1; k < kStages && i + k < filled; ++k)
         mbar_wait(smem_u32(&bars[warp][(i + k) % kStages]), (phases >> ((i + k) % kStages)) & 1, &g_status_attn, kSiteWait);
       break;
     }
     phases ^= 1u << stage;
-    const uint32_t base = ring + stage * kStage;
-    const uint32_t kc = base, vc = base + kCodes, kp = base + 2 * kCodes, vp = kp + kParams;
+    const uint8_t* base = smem + (warp * kStages + stage) * kStage;
+    const uint8_t *kc = base, *vc = base + kCodes, *kp = base + 2 * kCodes, *vp = kp + kParams;
     const int t0 = (use.s.c0 + use.c) * kChunk;
     auto tiles = [&](auto all) {  // all: every row sees every key
       constexpr bool kAll = decltype(all)::value;
-#pragma unroll 2
-      for (int tile = 0; tile < kTiles; ++tile) {
-        // scores
-        uint32_t kw[2][2 * G], pw[2][G], vw[2][G];
+#pragma unroll 1
+      for (int step = 0; step < kChunk / 32; ++step) {  // two tiles of 16 keys
+        float x[2][NT][4];
+        uint32_t vw[2][2][G];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int tok = tile * 16 + hh * 8 + kt;
-          lds(kw[hh], kc + tok * (D / 2) + q4 * (8 * G));
-          lds(pw[hh], kp + tok * (G * 4));
-          lds(vw[hh], vp + tok * (G * 4));
-        }
-        float x[NT][G][4];
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const int tile = 2 * step + i2;
+          // scores
+          uint32_t kw[2][2 * G], pw[2][G];
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const uint32_t u = kw[0][jj * G + g], v = kw[1][jj * G + g];
-            const uint32_t us = u >> 8, vs = v >> 8;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (jj == 0)
-                mma16816_zero(x[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
-                              qf[nt][g][jj][0], qf[nt][g][jj][1]);
-              else
-                mma16816(x[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
-                         qf[nt][g][jj][0], qf[nt][g][jj][1]);
-              mma16816(x[nt][g], us & 0x000F000Fu, vs & 0x000F000Fu, us & 0x00F000F0u, vs & 0x00F000F0u,
-                       qf[nt][g][jj][2], qf[nt][g][jj][3]);
-            }
+          for (int hh = 0; hh < 2; ++hh) {
+            const int tok = tile * 16 + hh * 8 + kt;
+            lds(kw[hh], kc + tok * (D / 2) + q4 * (8 * G));
+            lds(pw[hh], kp + tok * (G * 4));
+            lds(vw[i2][hh], vp + tok * (G * 4));
           }
+          float acc[NT][G][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float2 so[G];
-#pragma unroll
-          for (int g = 0; g < G; ++g) so[g] = half2_f32(pw[k >> 1][g]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float v = so[0].y * qs[nt][k & 1][0];
+          for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              if (g > 0) v = fmaf(so[g].y, qs[nt][k & 1][g], v);
-              v = fmaf(x[nt][g][k], so[g].x, v);
+              const uint32_t u = kw[0][jj * G + g], v = kw[1][jj * G + g];
+              const uint32_t us = u >> 8, vs = v >> 8;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (jj == 0)
+                  mma16816_zero(acc[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                                qf[nt][g][jj][0], qf[nt][g][jj][1]);
+                else
+                  mma16816(acc[nt][g], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u,
+                           qf[nt][g][jj][0], qf[nt][g][jj][1]);
+                mma16816(acc[nt][g], us & 0x000F000Fu, vs & 0x000F000Fu, us & 0x00F000F0u, vs & 0x00F000F0u,
+                         qf[nt][g][jj][2], qf[nt][g][jj][3]);
+              }
             }
-            if constexpr (!kAll) {
-              const int t = t0 + tile * 16 + (k >> 1) * 8 + kt;
-              if (t < beg[nt][k & 1] || t >= end[nt][k & 1]) v = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float2 so[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) so[g] = half2_f32(pw[k >> 1][g]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float v = so[0].y * qs[nt][k & 1][0];
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+                if (g > 0) v = fmaf(so[g].y, qs[nt][k & 1][g], v);
+                v = fmaf(acc[nt][g][k], so[g].x, v);
+              }
+              if constexpr (!kAll) {
+                const int t = t0 + tile * 16 + (k >> 1) * 8 + kt;
+                if (t < beg[nt][k & 1] || t >= end[nt][k & 1]) v = -INFINITY;
+              }
+              x[i2][nt][k] = v;
             }
-            x[nt][0][k] = v;
           }
         }
 
         // does a score pass the maximum too far, or a scale (of a key that any row sees) what kappa holds?
         uint32_t smax = 0;
+        float e[2][NT][4], far = -INFINITY;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int t = t0 + tile * 16 + hh * 8 + kt;
-          if (kAll || (t >= use.s.lo && t < use.s.len)) {
+        for (int i2 = 0; i2 < 2; ++i2) {
 #pragma unroll
-            for (int g = 0; g < G; ++g) smax = max_halves(smax, vw[hh][g]);
+          for (int hh = 0; hh < 2; ++hh) {
+            const int t = t0 + (2 * step + i2) * 16 + hh * 8 + kt;
+            if (kAll || (t >= use.s.lo && t < use.s.len)) {
+#pragma unroll
+              for (int g = 0; g < G; ++g) smax = max_halves(smax, vw[i2][hh][g]);
+            }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float v = x[i2][nt][k];
+              e[i2][nt][k] = kAll || v != -INFINITY ? fmaf(v, sigma[nt][k & 1], mneg[nt][k & 1]) : -INFINITY;
+              far = fmaxf(far, e[i2][nt][k]);
+            }
         }
         smax &= 0x7FFFu;  // fp16 bits order like the values (a scale is not negative)
-        float e[NT][4], far = -INFINITY;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            e[nt][k] = kAll || x[nt][0][k] != -INFINITY ? fmaf(x[nt][0][k], sigma[nt][k & 1], mneg[nt][k & 1]) : -INFINITY;
-            far = fmaxf(far, e[nt][k]);
-          }
         if (__any_sync(0xffffffffu, far > lift + kAhead || smax > limit)) {
           smax = min(__reduce_max_sync(0xffffffffu, smax), 0x7BFFu);
           float shift = lift;
@@ -667,7 +706,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float t = fmaxf(m[nt][c], fmaxf(x[nt][0][c], x[nt][0][2 + c]));
+              float t = fmaxf(fmaxf(m[nt][c], fmaxf(x[0][nt][c], x[0][nt][2 + c])), fmaxf(x[1][nt][c], x[1][nt][2 + c]));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
               const float safe = t == -INFINITY ? 0.0f : t;
@@ -676,7 +715,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
               const float mn = fmaf(-safe, sigma[nt][c], lift);
               mneg[nt][c] = t == -INFINITY ? INFINITY : mn;
 #pragma unroll
-              for (int k = c; k < 4; k += 2) e[nt][k] = fmaf(x[nt][0][k], sigma[nt][c], mn);
+              for (int i2 = 0; i2 < 2; ++i2)
+#pragma unroll
+                for (int k = c; k < 4; k += 2) e[i2][nt][k] = fmaf(x[i2][nt][k], sigma[nt][c], mn);
               l[nt][c] *= corr;
 #pragma unroll
               for (int g = 0; g < G; ++g) {
@@ -691,60 +732,65 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
         }
 
         // probabilities (times kappa) and the second product
-        uint32_t pf[NT][G][2];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float2 so[G];
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const int tile = 2 * step + i2;
+          uint32_t pf[NT][G][2];
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            so[g] = half2_f32(vw[hh][g]);
-            so[g].y = fmaf(8.0f, so[g].x, so[g].y);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float p[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              p[c] = ex2(e[nt][2 * hh + c]);
-              l[nt][c] += p[c];
-            }
+          for (int hh = 0; hh < 2; ++hh) {
+            float2 so[G];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              float ps[2];
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                if (kAll || x[nt][0][2 * hh + c] != -INFINITY) {  // a hidden key's params may be anything
-                  ps[c] = p[c] * so[g].x;
-                  ob[nt][c][g] = fmaf(p[c], so[g].y, ob[nt][c][g]);
-                } else {
-                  ps[c] = 0.0f;
-                }
-              }
-              pf[nt][g][hh] = transpose8x8(half2_bits(ps[0], ps[1]));
+              so[g] = half2_f32(vw[i2][hh][g]);
+              so[g].y = fmaf(8.0f, so[g].x, so[g].y);
             }
-          }
-        }
-        uint32_t v0[2][G], v1[2][G];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          lds(v0[hh], vc + (tile * 16 + hh * 8 + vt0) * (D / 2) + r8 * (4 * G));
-          lds(v1[hh], vc + (tile * 16 + hh * 8 + vt1) * (D / 2) + r8 * (4 * G));
-        }
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // nibbles 0..3, 4..7
-            const uint32_t sel = half ? 0x7632u : 0x5410u;
-            const uint32_t e0 = __byte_perm(v0[0][g], v1[0][g], sel), e1 = __byte_perm(v0[1][g], v1[1][g], sel);
-            const uint32_t f0 = e0 >> 8, f1 = e1 >> 8;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816(o[nt][g][2 * half], e0 & 0x000F000Fu, f0 & 0x000F000Fu, e1 & 0x000F000Fu, f1 & 0x000F000Fu,
-                       pf[nt][g][0], pf[nt][g][1]);
-              mma16816(o[nt][g][2 * half], kMinus8, kMinus8, kMinus8, kMinus8, pf[nt][g][0], pf[nt][g][1]);
-              mma16816(o[nt][g][2 * half + 1], e0 & 0x00F000F0u, f0 & 0x00F000F0u, e1 & 0x00F000F0u, f1 & 0x00F000F0u,
-                       pf[nt][g][0], pf[nt][g][1]);
-              mma16816(o[nt][g][2 * half + 1], kMinus128, kMinus128, kMinus128, kMinus128, pf[nt][g][0], pf[nt][g][1]);
+              float p[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                p[c] = ex2(e[i2][nt][2 * hh + c]);
+                l[nt][c] += p[c];
+              }
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+                float ps[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  if (kAll || x[i2][nt][2 * hh + c] != -INFINITY) {  // a hidden key's params may be anything
+                    ps[c] = p[c] * so[g].x;
+                    ob[nt][c][g] = fmaf(p[c], so[g].y, ob[nt][c][g]);
+                  } else {
+                    ps[c] = 0.0f;
+                  }
+                }
+                pf[nt][g][hh] = transpose8x8(half2_bits(ps[0], ps[1]));
+              }
+            }
+          }
+          uint32_t v0[2][G], v1[2][G];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            lds(v0[hh], vc + (tile * 16 + hh * 8 + vt0) * (D / 2) + r8 * (4 * G));
+            lds(v1[hh], vc + (tile * 16 + hh * 8 + vt1) * (D / 2) + r8 * (4 * G));
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // nibbles 0..3, 4..7
+              const uint32_t sel = half ? 0x7632u : 0x5410u;
+              const uint32_t e0 = __byte_perm(v0[0][g], v1[0][g], sel), e1 = __byte_perm(v0[1][g], v1[1][g], sel);
+              const uint32_t f0 = e0 >> 8, f1 = e1 >> 8;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816(o[nt][g][2 * half], e0 & 0x000F000Fu, f0 & 0x000F000Fu, e1 & 0x000F000Fu, f1 & 0x000F000Fu,
+                         pf[nt][g][0], pf[nt][g][1]);
+                mma16816(o[nt][g][2 * half], kMinus8, kMinus8, kMinus8, kMinus8, pf[nt][g][0], pf[nt][g][1]);
+                mma16816(o[nt][g][2 * half + 1], e0 & 0x00F000F0u, f0 & 0x00F000F0u, e1 & 0x00F000F0u,
+                         f1 & 0x00F000F0u, pf[nt][g][0], pf[nt][g][1]);
+                mma16816(o[nt][g][2 * half + 1], kMinus128, kMinus128, kMinus128, kMinus128, pf[nt][g][0],
+                         pf[nt][g][1]);
+              }
             }
           }
         }
@@ -753,123 +799,92 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
     if (t0 >= max_beg && t0 + kChunk <= min_end) tiles(std::true_type{});
     else tiles(std::false_type{});
 
-    // refill the stage
     __syncwarp();
-    if (i + kStages < units) {
-      issue(stage);
-      if (i + kStages + 1 < units) {
-        fill.next(a);
-        look_up();
-      }
-    }
     // the item's end, or the worker's
-    const bool item_done = use.c + 1 == use.s.chunks;
-    if (item_done || i + 1 == units) end_item(item_done && starts_item);
-    if (i + 1 < units) {
-      use.next(a);
-      if (item_done) begin_item();
-    }
+    new_item = use.c + 1 == use.s.chunks;
+    if (new_item || i + 1 == units) end_item(new_item && starts_item);
+    if (i + 1 < units) use.next(a);
   }
+
   // --- what the warps left unfinished -----------------------------------------
   // In list order: each warp's continued item, then the one it started.  A group of parts that belong together
   // begins with a started item (or the CTA's first part) and takes every continued one up to the item's end.
   __syncthreads();
   const float* base = scratch.warp_parts + (int64_t)blockIdx.x * kWarps * 2 * part_floats(NT, D);
-  int groups = 0;
-  Crossing cross = {0, 0, 0, 0};
-  for (int i = 0; i < 2 * split.act;) {
-    const int kind = i & 1 ? left[i / 2].tail : left[i / 2].head;
-    if (kind == 0) {
-      ++i;
-      continue;
+  // bit w: warp w's head, a head that ends its item, a tail
+  const int kind = lane < kWarps ? left[lane].head : 0;
+  const uint32_t heads = __ballot_sync(0xffffffffu, kind != 0), done = __ballot_sync(0xffffffffu, kind == 2);
+  const uint32_t tails = __ballot_sync(0xffffffffu, lane < kWarps && left[lane].tail != 0);
+  // groups: the first warp's head (if it goes on from another CTA), and every tail; group k is warp (k mod warps)'s
+  const uint32_t starts_at = tails << 1 | (heads & 1);  // bit 0: that head, bit w + 1: warp w's tail
+  const int last = 31 - __clz(tails);                   // the only item that can leave the CTA starts here
+  const bool crosses = tails != 0 && (done >> (last + 1)) == 0;
+  if (tid == 0) {
+    Crossing cross = {0, 0, 0, 0};
+    if (crosses)
+      cross = {left[last].tail_b, left[last].tail_h, (int)(ctas.taker(left[last].tail_last) - blockIdx.x) + 1, 0};
+    scratch.crossing[blockIdx.x] = cross;
+  }
+  if (alone) return;
+#pragma unroll 1
+  for (int k = warp; k <= kWarps; k += kWarps) {
+    if (!(starts_at >> k & 1)) continue;
+    const bool starts = k > 0;
+    const int w0 = starts ? k - 1 : 0;  // the group's first part is this warp's
+    // the heads that follow: up to the first that ends the item, all of them without a gap
+    const uint32_t after = heads >> (w0 + 1), stop = done >> (w0 + 1);
+    bool ends = !starts && (done & 1);
+    int count = 1;
+    if (!ends) {
+      const int run = __ffs(~after) - 1, until = stop ? __ffs(stop) : 33;
+      ends = until <= run;
+      count += min(run, until);
     }
-    const bool starts = i & 1;
-    const int b = starts ? left[i / 2].tail_b : left[i / 2].head_b, h = starts ? left[i / 2].tail_h : left[i / 2].head_h;
-    const int from = i;
-    bool ends = !starts && kind == 2;
-    int count = 1, last = i;  // parts at from, then heads (even places) up to last
-    for (i = (i | 1) + 1; !ends && i < 2 * split.act; i += 2) {
-      if (left[i / 2].head == 0) {
-        if (left[i / 2].tail) break;  // cannot be: an item in progress is continued first
-        continue;                     // a worker without units
-      }
-      ++count;
-      last = i;
-      ends = left[i / 2].head == 2;
-    }
-    // the search goes on behind the last head taken: its own warp may have started another item
-    i = last + 1;
-    if (starts && !ends) cross = {b, h, split.worker_of(left[from / 2].tail_last) / split.act - (int)blockIdx.x + 1, 0};
+    const int b = starts ? left[w0].tail_b : left[w0].head_b, h = starts ? left[w0].tail_h : left[w0].head_h;
     int first, n, len;
     attn4_sequence(a, b, first, n, len);
-    float* to = scratch.cta_parts + (int64_t)(blockIdx.x * 2 + starts) * part_floats(NT, D);
-    for (int row = (warp + groups) % kWarps; row < n * a.group; row += kWarps) {
-      float v[D / 32];
-      int place = from;
-      const float2 tl = add_parts<D, NT>(
-          [&](int k) -> const float* {  // called in order: the heads behind `from` that hold a part
-            if (k > 0)
-              do place = (place | 1) + 1;
-              while (left[place / 2].head == 0);
-            return base + (int64_t)place * part_floats(NT, D);
-          },
-          count, row, lane, v);
-      if (starts && ends) {
-        write_row<D>(a, first + row / a.group, h * a.group + row % a.group, lane, v, tl.x, tl.y);
-      } else {
-        if constexpr (G == 2) *reinterpret_cast<float4*>(to + row * D + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
-        else *reinterpret_cast<float2*>(to + row * D + 2 * lane) = make_float2(v[0], v[1]);
-        if (lane == 0) *reinterpret_cast<float2*>(to + 8 * NT * D + 2 * row) = tl;
-      }
+#pragma unroll 1
+    for (int row0 = 0; row0 < n * a.group; row0 += 8) {
+      float v[8][D / 32], top, l;
+      add_parts<D, NT>(
+          [&](int i) { return base + (int64_t)(i == 0 ? 2 * w0 + starts : 2 * (w0 + i)) * part_floats(NT, D); }, count,
+          row0, lane, top, l, v);
+      if (starts && ends) write_rows<D>(a, first, h, row0, n * a.group, lane, top, l, v);
+      else
+        write_part<D, NT>(scratch.cta_parts + (int64_t)(blockIdx.x * 2 + starts) * part_floats(NT, D), row0, lane, top, l, v);
     }
-    ++groups;
   }
-  if (tid == 0) scratch.crossing[blockIdx.x] = cross;
 }
 
-// Joins the parts of the (sequence, head)s that cross CTAs: block (row, CTA in which it starts), the CTAs' parts
+// Joins the parts of the (sequence, head)s that cross CTAs: block (8 rows, CTA in which it starts), the CTAs' parts
 // in eight strands that are then added in order.
 template <int D, int NT>
 __global__ void __launch_bounds__(256)
     attention_kv4_join(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch) {
-  constexpr int V = D / 32;
-  __shared__ __align__(16) float sums[8][D];
-  __shared__ float2 tls[8];
+  __shared__ __align__(16) float strands[8][part_floats(1, D)];
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, cta = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int row0 = blockIdx.x * 8, cta = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const Crossing c = scratch.crossing[cta];
   if (c.ctas == 0) return;
   int first, n, len;
   attn4_sequence(a, c.b, first, n, len);
-  if (row >= n * a.group) return;
-  const int each = (c.ctas + 7) / 8, from = warp * each;
-  float v[V];
-  float2 tl = add_parts<D, NT>(
-      [&](int i) -> const float* {
-        const int k = from + i;
-        return scratch.cta_parts + (int64_t)((cta + k) * 2 + (k == 0)) * part_floats(NT, D);
-      },
-      max(0, min(each, c.ctas - from)), row, lane, v);
-#pragma unroll
-  for (int k = 0; k < V; ++k) sums[warp][V * lane + k] = v[k];
-  if (lane == 0) tls[warp] = tl;
+  if (row0 >= n * a.group) return;
+  const int each = (c.ctas + 7) / 8, from = warp * each, used = (c.ctas + each - 1) / each;
+  float v[8][D / 32], top, l;
+  if (warp < used) {
+    add_parts<D, NT>(
+        [&](int i) {
+          const int k = from + i;
+          return scratch.cta_parts + (int64_t)((cta + k) * 2 + (k == 0)) * part_floats(NT, D);
+        },
+        min(each, c.ctas - from), row0, lane, top, l, v);
+    write_part<D, 1>(strands[warp], 0, lane, top, l, v);
+  }
   __syncthreads();
   if (warp != 0) return;
-  float top = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, tls[i].x);
-  const float safe = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-  for (int k = 0; k < V; ++k) v[k] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = ex2(tls[i].x - safe);
-    l = fmaf(tls[i].y, f, l);
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = fmaf(sums[i][V * lane + k], f, v[k]);
-  }
-  write_row<D>(a, first + row / a.group, c.h * a.group + row % a.group, lane, v, top, l);
+  add_parts<D, 1>([&](int i) { return (const float*)strands[i]; }, used, 0, lane, top, l, v);
+  write_rows<D>(a, first, c.h, row0, n * a.group, lane, top, l, v);
 }
 
 size_t crossing_bytes() { return (size_t)sm_count() * sizeof(Crossing); }
@@ -893,7 +908,7 @@ qg_status launch(const Attn4& a, void* workspace, cudaStream_t s) {
   LaunchCfg lc((unsigned)grid, 32 * kWarps, kMost, s);
   cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_decode<G, NT>, a, scratch);
   if (e != cudaSuccess) return check_cuda(e, "attention_kv4 decode launch");
-  LaunchCfg lj((unsigned)std::min(8 * NT, a.q_starts ? 8 * NT : a.n_uniform * a.group), 256, 0, s);
+  LaunchCfg lj(NT, 256, 0, s);
   lj.cfg.gridDim.y = (unsigned)grid;
   e = cudaLaunchKernelEx(&lj.cfg, attention_kv4_join<D, NT>, a, scratch);
   return check_cuda(e, "attention_kv4 join launch");
