@@ -1,0 +1,805 @@
+// qg_attn_kv4_prompt.cu -- attention of many query rows over the paged 4-bit
+// cache: (sequence, KV head)s with more query tokens times head group than the
+// decode kernel takes (prompts, chunks of prompts, long drafts).
+//
+// Compute-bound: 4 dim operations and one exponential per (row, key).  One CTA
+// takes 256 rows (two tiles of 128) of a (sequence, KV head) and walks over the
+// keys 128 at a time:
+//   loader warp      packed codes and params of 64 tokens a stage, bulk copies
+//   4 warps          codes -> fp16 (c s + o, one rounding) into the swizzled
+//                    K-major operands K [key][channel] and V^T [channel][key];
+//                    both row tiles share them
+//   MMA warp         tcgen05: S = Q K^T (M 128, N 128, K dim) and O += P V
+//                    (P from tensor memory, N dim), accumulators in tensor memory
+//   2 x 4 warps      softmax of a row tile, a thread per row: maximum, p =
+//                    2^(x - m), P in fp16 over S's columns
+// While the tensor cores work for one row tile, the other's softmax runs.  The
+// maximum that scores are taken against moves only when a row passes it by 8
+// binary digits, so the accumulator is rarely rescaled; p carries a factor 2^7
+// that keeps small ones out of fp16's subnormals (p 2^7 < 2^15).
+//
+// Channels of K and Q lie in the order 0 4 1 5 2 6 3 7 of each 8 (the order in
+// which masks take nibbles from a word); row 8 i + j of a V^T group is channel
+// 8 j + i, which spreads the stores over the banks; the epilogue puts the
+// output's columns back.
+//
+// With few (rows, head)s the keys are split over CTAs whose parts a second
+// kernel joins in order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qg_device.cuh"
+#include "qg_internal.h"
+#include "qg_kv4.cuh"
+
+namespace qg {
+
+static __device__ unsigned long long g_status_prompt;
+
+unsigned long long read_clear_status_prompt(cudaStream_t s) {
+  unsigned long long v = 0, z = 0;
+  cudaMemcpyFromSymbolAsync(&v, g_status_prompt, sizeof(v), 0, cudaMemcpyDeviceToHost, s);
+  cudaMemcpyToSymbolAsync(g_status_prompt, &z, sizeof(z), 0, cudaMemcpyHostToDevice, s);
+  cudaStreamSynchronize(s);
+  return v;
+}
+
+namespace {
+
+constexpr int kRows = 256;      // query rows per CTA, two tiles of 128
+constexpr int kKeys = 128;      // keys per step
+constexpr int kHalf = 64;       // tokens per raw stage
+constexpr int kRaw = 3;         // raw stages
+constexpr int kThreads = 448;
+constexpr int kDequantWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
+constexpr float kLift = 7.0f, kAhead = 8.0f;
+
+enum : uint32_t {
+  kSiteSequence = 1, kSitePage, kSiteRawFull, kSiteRawEmpty, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty,
+  kSiteS, kSiteP, kSiteO, kSiteDrain
+};
+
+__device__ __forceinline__ void report(uint32_t code, uint32_t site) {
+  atomicCAS(&g_status_prompt, 0ull,
+            (unsigned long long)code | ((unsigned long long)site << 8) | ((unsigned long long)blockIdx.x << 24));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half2_f32(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// each half held to +-65504; a NaN becomes 65504
+__device__ __forceinline__ uint32_t h2_finite(uint32_t a) {
+  uint32_t d;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0x7BFF7BFFu));
+  asm("max.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0xFBFFFBFFu));
+  return d;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+      "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Codes of nibbles 0..3 of each half of w as fp16 pairs 0 (nibble 0 of both halves) .. 3, exact
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&c)[4]) {
+  const uint32_t w8 = w >> 8;
+  c[0] = h2_add((w & 0x000F000Fu) | 0x64006400u, 0xE400E400u);                  // 1024 + c, less 1024
+  c[1] = h2_fma((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);     // (1024 + 16 c) / 16 - 64
+  c[2] = h2_add((w8 & 0x000F000Fu) | 0x64006400u, 0xE400E400u);
+  c[3] = h2_fma((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
+}
+
+// Is the largest code's value not a finite fp16 (params that are not finite, or a value beyond the type)?
+__device__ __forceinline__ bool odd_params(uint32_t p) {
+  const __half2 so = *reinterpret_cast<__half2*>(&p);
+  const __half top = __hfma(__low2half(so), __float2half(15.0f), __high2half(so));
+  return (__half_as_ushort(top) & 0x7C00u) == 0x7C00u;
+}
+
+struct Job {
+  int b, h, tile, split;      // sequence, KV head, 256-row tile, share of the keys
+  int first, n, len, rows;    // the sequence
+};
+
+// Which rows a block works on; tiles in descending order, so that a causal mask's longest start first.
+__device__ __forceinline__ bool find_job(const Attn4& a, int min_rows, int splits, int block, int lane, Job& j) {
+  j.h = block % a.cache.heads;
+  block /= a.cache.heads;
+  j.split = block % splits;
+  block /= splits;
+  if (!a.q_starts) {
+    const int per = (a.n_uniform * a.group + kRows - 1) / kRows;
+    j.b = block % a.B;
+    j.tile = per - 1 - block / a.B;
+    if (j.tile < 0) return false;
+  } else {
+    int base = 0, at = 0;
+    j.b = -1;
+    for (; base < a.B; base += 32) {  // the whole warp
+      int first, n = 0, len, tiles = 0;
+      if (base + lane < a.B) {
+        attn4_sequence(a, base + lane, first, n, len);
+        if (n * a.group >= min_rows) tiles = (n * a.group + kRows - 1) / kRows;
+      }
+      int scan = tiles;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, scan, d);
+        if (lane >= d) scan += v;
+      }
+      const uint32_t found = __ballot_sync(0xffffffffu, block < at + scan);
+      if (found) {
+        const int src = __ffs(found) - 1;
+        j.b = base + src;
+        const int before = at + __shfl_sync(0xffffffffu, scan - tiles, src);
+        j.tile = __shfl_sync(0xffffffffu, tiles, src) - 1 - (block - before);
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, scan, 31);
+    }
+    if (j.b < 0) return false;
+  }
+  attn4_sequence(a, j.b, j.first, j.n, j.len);
+  j.rows = j.n * a.group;
+  return true;
+}
+
+template <int G>
+struct Layout {
+  static constexpr int D = 64 * G;
+  static constexpr uint32_t kBlock = 128 * 128;                 // 128 rows of 128 bytes
+  static constexpr uint32_t kOperand = G * kBlock;              // 128 x D fp16
+  static constexpr uint32_t q = 0;                              // [2 tiles]
+  static constexpr uint32_t k = 2 * kOperand;                   // [2 buffers] [G][128 keys][64 channels]
+  static constexpr uint32_t v = 4 * kOperand;                   // [2 buffers] [2][D rows][64 keys]
+  static constexpr uint32_t raw = 6 * kOperand;                 // [kRaw]
+  static constexpr uint32_t kCodes = kHalf * D / 2, kParams = kHalf * G * 4;
+  static constexpr uint32_t kStage = 2 * (kCodes + kParams);
+  static constexpr uint32_t bytes = raw + kRaw * kStage;
+};
+
+// A part of a row for the join: D sums, then (log2 maximum, sum).
+template <int G>
+struct Parts {
+  float* sums;  // [splits][T heads_q][D]
+  float2* ml;   // [splits][T heads_q]
+};
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_kv4_prompt(const __grid_constant__ Attn4 a, int min_rows, int splits, const Parts<G> parts) {
+  using L = Layout<G>;
+  constexpr int D = L::D;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2],
+      s_full[2], p_full[2], o_done[2], drained;
+  __shared__ uint32_t tmem_slot;
+  const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smp = smem_raw + (sm - smem_u32(smem_raw));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+
+  if (tid == 0) {
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(smem_u32(&raw_full[i]), 1);
+      mbar_init(smem_u32(&raw_empty[i]), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&k_full[i]), 4);
+      mbar_init(smem_u32(&k_empty[i]), 1);
+      mbar_init(smem_u32(&v_full[i]), 4);
+      mbar_init(smem_u32(&v_empty[i]), 1);
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 128);
+      mbar_init(smem_u32(&o_done[i]), 1);
+    }
+    mbar_init(smem_u32(&drained), 1);
+    fence_mbar_init();
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0)
+    for (int b = tid; b < a.B; b += kThreads) {
+      int f, n, l;
+      if (!attn4_sequence(a, b, f, n, l)) report(kDevBadArg, kSiteSequence);
+    }
+  Job job;
+  if (!find_job(a, min_rows, splits, blockIdx.x, lane, job)) return;  // the same for every warp
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+
+  // the keys of each row tile, in steps from the CTA's first
+  const int row0 = job.tile * kRows;
+  const auto pos_of = [&](int row) { return job.len - job.n + row / a.group; };
+  const auto end_of = [&](int row) { return max(0, a.causal ? min(job.len, pos_of(row) + 1) : job.len); };
+  const auto beg_of = [&](int row) { return a.window > 0 ? max(0, pos_of(row) - a.window + 1) : 0; };
+  const int step0 = min(beg_of(row0), job.len) / kKeys;
+  int steps[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(row0 + 128 * t + 127, job.rows - 1);
+    steps[t] = row0 + 128 * t < job.rows ? max(0, (end_of(last) + kKeys - 1) / kKeys - step0) : 0;
+  }
+  const int all = max(steps[0], steps[1]);
+  const int j0 = (int)((int64_t)all * job.split / splits), j1 = (int)((int64_t)all * (job.split + 1) / splits);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) steps[t] = max(0, min(steps[t], j1) - j0);
+  const int total = max(steps[0], steps[1]);
+  const int first_step = step0 + j0;
+  const int lo = min(beg_of(row0), job.len);  // the oldest key that any row sees
+
+  // --- queries: a thread per row, scaled by a power of two to fp16 -------------
+  float sigma = 0.0f;
+  const int tile = warp / 4 & 1, row = row0 + tid;  // softmax warps
+  if (warp < kDequantWarp) {
+    uint4 v[D / 8];
+    float amax = 0.0f;
+    if (row < job.rows) {
+      const int t = job.first + row / a.group, hq = job.h * a.group + row % a.group;
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + 2 * (t * a.q_st + hq * a.q_sh));
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) v[i] = p[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    const auto values = [&](uint32_t b) {
+      return a.dtype == QG_F16 ? half2_f32(b) : make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+    };
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const uint32_t* pv = &v[i].x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = values(pv[k]);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    int e = 8 - ((int)(__float_as_uint(amax) >> 23) - 127);
+    e = max(-100, min(100, e));
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+    sigma = a.scale * 1.44269504088896f * __uint_as_float((uint32_t)(127 - e) << 23);
+    const uint32_t qrow = sm + L::q + tile * L::kOperand + (tid & 127) * 128;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const float2 f0 = values(v[i].x), f1 = values(v[i].y), f2 = values(v[i].z), f3 = values(v[i].w);
+      sts128(qrow + (i / 8) * L::kBlock + (((i & 7) ^ (tid & 7)) << 4), half2_bits(f0.x * up, f2.x * up),
+             half2_bits(f0.y * up, f2.y * up), half2_bits(f1.x * up, f3.x * up), half2_bits(f1.y * up, f3.y * up));
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  cta_barrier_all();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const uint32_t tm_s = tmem, tm_o = tmem + 256;  // S: 128 columns a tile; O: D columns a tile
+
+  if (warp == kLoadWarp) {
+    // ---- packed codes and params --------------------------------------------
+    const int P = a.cache.page_size;
+    const int piece = min(kHalf, P & -P), pieces = kHalf / piece;
+    const int arr = lane / pieces, pc = lane % pieces;
+    const uint32_t bytes = arr < 2 ? piece * (D / 2) : piece * (G * 4);
+    const uint32_t dst_off = (arr < 2 ? arr * L::kCodes : 2 * L::kCodes + (arr - 2) * L::kParams) + pc * bytes;
+    const uint32_t code_lanes = (1u << (2 * pieces)) - 1;
+    int issued = 0;
+#pragma unroll 1
+    for (int i = 0; i < 2 * total; ++i) {
+      int page = -1, in_page = 0;
+      const int t = first_step * kKeys + i * kHalf + pc * piece;
+      if (arr < 4 && t < job.len) {
+        const int pi = (int)(((uint64_t)(uint32_t)(t >> 4) * a.page_magic) >> 40);
+        in_page = t - pi * P;
+        page = __ldg(a.table + (int64_t)job.b * a.table_ld + pi);
+        if (page < 0 || page >= a.cache.pages) {
+          report(kDevBadArg, kSitePage);
+          page = -1;
+        }
+      }
+      const int st = i % kRaw;
+      if (!mbar_wait(smem_u32(&raw_empty[st]), (i / kRaw & 1) ^ 1, &g_status_prompt, kSiteRawEmpty)) break;
+      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+      const uint32_t bar = smem_u32(&raw_full[st]);
+      if (lane == 0)
+        mbar_arrive_expect_tx(bar, __popc(have & code_lanes) * (uint32_t)(piece * (D / 2)) +
+                                       __popc(have & ~code_lanes) * (uint32_t)(piece * (G * 4)));
+      __syncwarp();
+      if (page >= 0) {
+        const int64_t r = kv4_row(a.cache, page, job.h) + in_page;
+        const uint32_t* src = arr < 2 ? (arr == 0 ? a.cache.codes[0] : a.cache.codes[1]) + r * (D / 8)
+                                      : (arr == 2 ? a.cache.params[0] : a.cache.params[1]) + r * G;
+        bulk_load(sm + L::raw + st * L::kStage + dst_off, src, bytes, bar);
+      }
+      issued = i + 1;
+    }
+    // no copy in flight outlives the CTA
+    for (int i = max(0, issued - kRaw); i < issued; ++i)
+      mbar_wait(smem_u32(&raw_full[i % kRaw]), i / kRaw & 1, &g_status_prompt, kSiteDrain);
+  } else if (warp == kMmaWarp) {
+    // ---- tensor cores ---------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys), kIdescO = idesc_f16_f32(128, D);
+      const auto scores = [&](int t, int buf) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16(tm_s + t * 128, sdesc_sw128(sm + L::q + t * L::kOperand + g * L::kBlock + k * 32),
+                    sdesc_sw128(sm + L::k + buf * L::kOperand + g * L::kBlock + k * 32), kIdescS, (g | k) != 0);
+        mma_commit(smem_u32(&s_full[t]));
+      };
+      const auto outputs = [&](int t, int buf, bool more) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ts(tm_o + t * D, tm_s + t * 128 + b * 32 + k * 8,
+                       sdesc_sw128(sm + L::v + buf * L::kOperand + b * (D * 128) + k * 32), kIdescO,
+                       more || (b | k) != 0);
+        mma_commit(smem_u32(&o_done[t]));
+      };
+      const auto wait = [&](uint64_t& bar, int parity, uint32_t site) {
+        const bool ok = mbar_wait(smem_u32(&bar), parity, &g_status_prompt, site);
+        tc_fence_after();
+        return ok;
+      };
+      bool ok = true;
+      if (total > 0) {
+        ok = wait(k_full[0], 0, kSiteKFull);
+        if (ok) {
+          for (int t = 0; t < 2; ++t)
+            if (steps[t] > 0) scores(t, 0);
+          mma_commit(smem_u32(&k_empty[0]));
+        }
+      }
+#pragma unroll 1
+      for (int j = 0; j < total && ok; ++j) {
+        const int buf = j & 1, par = j >> 1 & 1;
+        ok = wait(v_full[buf], par, kSiteVFull);
+        if (ok && j + 1 < total) ok = wait(k_full[buf ^ 1], (j + 1) >> 1 & 1, kSiteKFull);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && j < steps[t]) {
+            ok = wait(p_full[t], j & 1, kSiteP);
+            if (!ok) break;
+            outputs(t, buf, j > 0);
+            // in order behind the product that reads P from the same columns
+            if (j + 1 < steps[t]) scores(t, buf ^ 1);
+          }
+        mma_commit(smem_u32(&v_empty[buf]));
+        if (j + 1 < total) mma_commit(smem_u32(&k_empty[buf ^ 1]));
+      }
+      mma_commit(smem_u32(&drained));
+      mbar_wait(smem_u32(&drained), 0, &g_status_prompt, kSiteDrain);
+    }
+    __syncwarp();
+  } else if (warp >= kDequantWarp) {
+    // ---- codes to fp16 ----------------------------------------------------------
+    const int dt = tid - 32 * kDequantWarp;
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < 2 * total && ok; ++i) {
+      const int j = i >> 1, half = i & 1, buf = j & 1, st = i % kRaw;
+      if (half == 0) {
+        ok = mbar_wait(smem_u32(&k_empty[buf]), (j >> 1 & 1) ^ 1, &g_status_prompt, kSiteKEmpty) &&
+             mbar_wait(smem_u32(&v_empty[buf]), (j >> 1 & 1) ^ 1, &g_status_prompt, kSiteVEmpty);
+        if (!ok) break;
+      }
+      ok = mbar_wait(smem_u32(&raw_full[st]), i / kRaw & 1, &g_status_prompt, kSiteRawFull);
+      if (!ok) break;
+      const uint8_t* raw = smp + L::raw + st * L::kStage;
+      const uint8_t *kc = raw, *vc = raw + L::kCodes, *kp = raw + 2 * L::kCodes, *vp = kp + L::kParams;
+      const int t0 = (first_step + j) * kKeys + half * kHalf;
+
+      // keys: a lane takes 4 words (32 channels) of one token
+      constexpr int kParts = D / 32;  // lanes per token
+#pragma unroll
+      for (int it = 0; it < kParts / 2; ++it) {
+        const int item = dt + 128 * it, part = item % kParts, tok = item / kParts;
+        // the warp's tokens: is any value of theirs not an fp16?
+        uint32_t kpw[G], vpw[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          kpw[g] = *reinterpret_cast<const uint32_t*>(kp + (tok * G + g) * 4);
+          vpw[g] = *reinterpret_cast<const uint32_t*>(vp + (tok * G + g) * 4);
+        }
+        bool odd = false;
+#pragma unroll
+        for (int g = 0; g < G; ++g) odd |= odd_params(kpw[g]) | odd_params(vpw[g]);
+        const uint4 words = *reinterpret_cast<const uint4*>(kc + tok * (D / 2) + part * 16);
+        const uint32_t* w = &words.x;
+        uint32_t out[4][4];
+        uint32_t s2[G], o2[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          s2[g] = __byte_perm(kpw[g], 0, 0x1010);
+          o2[g] = __byte_perm(kpw[g], 0, 0x3232);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t c[4];
+          codes_f16(w[k], c);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) out[k][m] = h2_fma(c[m], s2[k % G], o2[k % G]);
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+          // A value that is not finite makes the key NaN: every row that sees the token becomes NaN, none else
+          // (the value itself is taken finite below).  Large keys are held to the type.
+          bool bad = false;
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            bad |= (vpw[g] & 0x7C00u) == 0x7C00u || (vpw[g] & 0x7C000000u) == 0x7C000000u ||
+                   (kpw[g] & 0x7C00u) == 0x7C00u || (kpw[g] & 0x7C000000u) == 0x7C000000u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) out[k][m] = bad ? 0x7FFF7FFFu : h2_finite(out[k][m]);
+        }
+        // word k of the lane is word [j, g] of the token: index part * 4 + k = j G + g
+        const uint32_t krow = sm + L::k + buf * L::kOperand + (half * kHalf + tok) * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int jw = (part * 4 + k) / G;
+          sts128(krow + (k % G) * L::kBlock + ((jw ^ (tok & 7)) << 4), out[k][0], out[k][1], out[k][2], out[k][3]);
+        }
+      }
+      if (half == 1) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&k_full[buf]));
+      }
+
+      // values: a lane takes one word (8 channels) of 8 tokens and writes 8 tokens of 8 channels
+      if (G == 2 || dt < 64) {
+        const int jw = dt & 7, g = G == 2 ? dt >> 3 & 1 : 0, tg = dt >> (G == 2 ? 4 : 3);
+        const int swap = tg & 1;  // odd groups read their pairs the other way round: no bank twice
+        uint32_t pw[8];
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          pw[k] = *reinterpret_cast<const uint32_t*>(vp + ((tg * 8 + k) * G + g) * 4);
+          const int t = t0 + tg * 8 + k;
+          odd |= odd_params(pw[k]) || t < lo || t >= job.len;
+        }
+        const bool any = __any_sync(G == 2 ? 0xffffffffu : 0xffffffffu, odd);
+        if (any) {  // tokens that no row sees: zero
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int t = t0 + tg * 8 + k;
+            if (t < lo || t >= job.len) pw[k] = 0u;
+          }
+        }
+        uint32_t out[8][4];  // channel, token pair
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint8_t* src = vc + (tg * 8 + 2 * p) * (D / 2) + (jw * G + g) * 4;
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(src + swap * (D / 2));
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(src + (swap ^ 1) * (D / 2));
+          const uint32_t s2 = __byte_perm(pw[2 * p], pw[2 * p + 1], 0x5410);
+          const uint32_t o2 = __byte_perm(pw[2 * p], pw[2 * p + 1], 0x7632);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {  // nibbles 0..3, 4..7
+            uint32_t c[4];
+            codes_f16(__byte_perm(x, y, hh ? (swap ? 0x3276u : 0x7632u) : (swap ? 0x1054u : 0x5410u)), c);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) out[4 * hh + m][p] = h2_fma(c[m], s2, o2);
+          }
+        }
+        if (any) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) out[c][p] = h2_finite(out[c][p]);
+        }
+        // row 64 g + 8 i + jw, keys half * 64 + tg * 8 ..: block `half`, chunk tg
+        const uint32_t vrow = sm + L::v + buf * L::kOperand + half * (D * 128) + (64 * g + jw) * 128 + ((tg ^ jw) << 4);
+#pragma unroll
+        for (int i2 = 0; i2 < 8; ++i2) sts128(vrow + i2 * 8 * 128, out[i2][0], out[i2][1], out[i2][2], out[i2][3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&raw_empty[st]));
+      if (half == 1) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&v_full[buf]));
+      } else {
+        fence_proxy_async_smem();
+      }
+    }
+  } else {
+    // ---- softmax, one thread per row ------------------------------------------
+    const int mine = steps[tile];
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor-memory lane 32 (warp % 4)
+    const uint32_t ts = tm_s + tile * 128 + lanes, to = tm_o + tile * D + lanes;
+    const int last_row = min(row0 + 128 * tile + 127, job.rows - 1);
+    const int r = min(row, last_row);  // rows behind the last: zero queries with its mask
+    const int end = end_of(r), beg = beg_of(r);
+    const int min_end = end_of(row0 + 128 * tile), max_beg = beg_of(last_row);
+    float m = -INFINITY, mneg = 0.0f, l = 0.0f;  // the maximum taken against, kLift - m sigma, the sum of p 2^kLift
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; j < mine; ++j) {
+      ok = mbar_wait(smem_u32(&s_full[tile]), j & 1, &g_status_prompt, kSiteS);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const int t0 = (first_step + j) * kKeys;
+      const bool full = t0 >= max_beg && t0 + kKeys <= min_end;
+      const int cb = beg - t0, ce = end - t0;  // the visible columns [cb, ce)
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        tmem_ld32(ts + 32 * c, v);
+        tmem_ld_wait();
+        if (full) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i >= cb && 32 * c + i < ce) top = fmaxf(top, __uint_as_float(v[i]));
+        }
+      }
+      const bool far = top > -INFINITY && (m == -INFINITY || (top - m) * sigma > kAhead);
+      if (__any_sync(0xffffffffu, far)) {
+        const float mn = fmaxf(m, top);
+        const float corr = m == -INFINITY ? 0.0f : ex2((m - mn) * sigma);
+        m = mn;
+        mneg = m == -INFINITY ? 0.0f : fmaf(-m, sigma, kLift);
+        l *= corr;
+        if (j > 0) {
+          ok = mbar_wait(smem_u32(&o_done[tile]), (j - 1) & 1, &g_status_prompt, kSiteO);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(to + 16 * c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
+            tmem_st16(to + 16 * c, v);
+          }
+        }
+      }
+      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32], p[16];
+        tmem_ld32(ts + 32 * c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float x = ex2(fmaf(__uint_as_float(v[i]), sigma, mneg));
+          if (!full && (32 * c + i < cb || 32 * c + i >= ce)) x = 0.0f;
+          part[i & 3] += x;
+          v[i] = __float_as_uint(x);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = half2_bits(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        tmem_st16(ts + 16 * c, p);  // over columns that have been read
+      }
+      l += (part[0] + part[1]) + (part[2] + part[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&p_full[tile]));
+    }
+    // the output row
+    if (mine > 0 && ok) ok = mbar_wait(smem_u32(&o_done[tile]), (mine - 1) & 1, &g_status_prompt, kSiteO);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    const bool valid = row < job.rows;
+    const int t = job.first + row / a.group, hq = job.h * a.group + row % a.group;
+    const int64_t flat = (int64_t)job.split * a.T * a.heads_q + (int64_t)t * a.heads_q + hq;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float v[64];
+      if (mine > 0) {
+        uint32_t u[32];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          tmem_ld32(to + 64 * g + 32 * hh, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[32 * hh + i] = __uint_as_float(u[i]);
+        }
+      }
+      if (mine == 0 || l == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+      }
+      if (valid && ok) {
+        // column 8 i + jw is channel 8 jw + i
+        if (splits == 1) {
+          char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + 64 * g);
+#pragma unroll
+          for (int jw = 0; jw < 8; ++jw) {
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x = v[16 * i + jw] * inv, y = v[16 * i + 8 + jw] * inv;
+              if (a.dtype == QG_F16) {
+                b[i] = half2_bits(x, y);
+              } else {
+                __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                b[i] = *reinterpret_cast<uint32_t*>(&h);
+              }
+            }
+            *reinterpret_cast<uint4*>(p + 16 * jw) = make_uint4(b[0], b[1], b[2], b[3]);
+          }
+        } else {
+          float* p = parts.sums + flat * D + 64 * g;
+#pragma unroll
+          for (int jw = 0; jw < 8; ++jw) {
+            *reinterpret_cast<float4*>(p + 8 * jw) = make_float4(v[jw], v[8 + jw], v[16 + jw], v[24 + jw]);
+            *reinterpret_cast<float4*>(p + 8 * jw + 4) = make_float4(v[32 + jw], v[40 + jw], v[48 + jw], v[56 + jw]);
+          }
+        }
+      }
+    }
+    if (valid && ok) {
+      const float lg = l == 0.0f ? -INFINITY : m * sigma - kLift;  // log2 of what p was taken against
+      if (splits > 1) parts.ml[flat] = make_float2(lg, l);
+      else if (a.lse) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (lg + log2f(l)) * 0.69314718056f;
+    }
+    tc_fence_before();
+  }
+  cta_barrier_all();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the splits' parts: block (tile, head) as above, a warp per row.
+template <int G>
+__global__ void __launch_bounds__(256)
+    attention_kv4_prompt_join(const __grid_constant__ Attn4 a, int min_rows, int splits, const Parts<G> parts) {
+  constexpr int D = 64 * G, V = D / 32;
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  Job job;
+  if (!find_job(a, min_rows, 1, blockIdx.x, lane, job)) return;
+  const int64_t stride = (int64_t)a.T * a.heads_q;
+  const int row0 = job.tile * kRows + blockIdx.y * 32;
+#pragma unroll 1
+  for (int row = row0 + warp; row < min(row0 + 32, job.rows); row += 8) {
+    const int t = job.first + row / a.group, hq = job.h * a.group + row % a.group;
+    const int64_t flat = (int64_t)t * a.heads_q + hq;
+    float top = -INFINITY, l = 0.0f, v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < splits; ++i) {
+      const float2 ml = parts.ml[flat + i * stride];
+      float x[V];
+      const float* p = parts.sums + (flat + i * stride) * D + V * lane;
+      if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p);
+      else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p);
+      const float tn = fmaxf(top, ml.x), safe = tn == -INFINITY ? 0.0f : tn;
+      const float f = ex2(top - safe), g = ex2(ml.x - safe);
+      l = l * f + ml.y * g;
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = fmaf(x[k], g, v[k] * f);
+      top = tn;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t b[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float x = l == 0.0f ? 0.0f : v[2 * i] * inv, y = l == 0.0f ? 0.0f : v[2 * i + 1] * inv;
+      if (a.dtype == QG_F16) {
+        b[i] = half2_bits(x, y);
+      } else {
+        __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        b[i] = *reinterpret_cast<uint32_t*>(&h);
+      }
+    }
+    char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+    else *reinterpret_cast<uint32_t*>(p) = b[0];
+    if (a.lse && lane == 0) a.lse[flat] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
+  }
+}
+
+// Row tiles of a call (an upper bound where the sequences' row counts are on the device)
+int64_t row_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
+  return ragged ? T * group / kRows + B : B * ((T / B * group + kRows - 1) / kRows);
+}
+
+// Shares of the keys: as many as there are SMs for the (row tile, head)s, at most 32.
+int key_splits(int64_t tiles, int64_t heads) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(32, sm_count() / std::max<int64_t>(1, tiles * heads)));
+}
+
+template <int G>
+qg_status launch(const Attn4& a, int min_rows, void* workspace, cudaStream_t s) {
+  constexpr int kSmem = Layout<G>::bytes + 1024;
+  static PerDeviceOnce once;
+  const qg_status st = once.run([](int) {
+    return check_cuda(cudaFuncSetAttribute(attention_kv4_prompt<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+                      "attention_kv4 shared memory");
+  });
+  if (st != QG_OK) return st;
+  const int64_t tiles = row_tiles(a.B, a.T, a.group, a.q_starts != nullptr);
+  const int splits = key_splits(tiles, a.cache.heads);
+  if (tiles * a.cache.heads * splits >= ((int64_t)1 << 31)) return fail(QG_ERR_UNSUPPORTED, "attention_kv4: too many row tiles");
+  Parts<G> parts = {};
+  if (splits > 1) {
+    parts.sums = static_cast<float*>(workspace);
+    parts.ml = reinterpret_cast<float2*>(parts.sums + (int64_t)splits * a.T * a.heads_q * 64 * G);
+  }
+  LaunchCfg lc((unsigned)(tiles * a.cache.heads * splits), kThreads, kSmem, s);
+  cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt<G>, a, min_rows, splits, parts);
+  if (e != cudaSuccess || splits == 1) return check_cuda(e, "attention_kv4 prompt launch");
+  LaunchCfg lj((unsigned)(tiles * a.cache.heads), 256, 0, s);
+  lj.cfg.gridDim.y = kRows / 32;
+  e = cudaLaunchKernelEx(&lj.cfg, attention_kv4_prompt_join<G>, a, min_rows, splits, parts);
+  return check_cuda(e, "attention_kv4 prompt join launch");
+}
+
+// Rows (query tokens x head group) that the decode kernel takes, in tiles of 8; 0: none.  A ragged call gives it
+// the sequences of 8 rows at most (16 where one token has more than 8).
+int decode_tiles(int64_t n, int64_t group, bool ragged) {
+  const int64_t rows = ragged ? group : n * group;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t dim, bool ragged) {
+  const int64_t group = heads_q / heads;
+  const int nt = decode_tiles(T / B, group, ragged);
+  size_t bytes = nt ? round256(attention_kv4_decode_workspace(dim, nt)) : 0;
+  if (!nt || ragged) {
+    const int splits = key_splits(row_tiles(B, T, group, ragged), heads);
+    if (splits > 1) bytes += (size_t)splits * T * heads_q * (dim + 2) * sizeof(float);
+  }
+  return bytes;
+}
+
+// Single tokens and drafts go to the decode kernel, longer ones here; a ragged
+// call launches both and each takes its sequences.
+qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s) {
+  const int nt = decode_tiles(a.n_uniform, a.group, a.q_starts != nullptr);
+  if (nt) {
+    const qg_status st = launch_attention_kv4_decode(a, nt, workspace, s);
+    if (st != QG_OK || !a.q_starts) return st;
+    workspace = static_cast<char*>(workspace) + round256(attention_kv4_decode_workspace(a.cache.dim, nt));
+  }
+  return a.cache.dim == 64 ? launch<1>(a, 8 * nt + 1, workspace, s) : launch<2>(a, 8 * nt + 1, workspace, s);
+}
+
+}  // namespace qg

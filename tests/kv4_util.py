@@ -79,7 +79,7 @@ def paged(lens, page_size, seed, spare=2):
 # Attention
 # ---------------------------------------------------------------------------
 def attention_ref(q, cache, table, lens, new, scale, causal=True, window=0):
-    """fp64 (out [T, Hq, D], lse [T, Hq], bound [T, Hq, D]) of attention over the cache.
+    """fp64 (out [T, Hq, D], lse [T, Hq], bound [T, Hq, D], lse_bound [T, Hq]) of attention over the cache.
 
     bound: the arithmetic error that the kernels may make besides the output's rounding.
     With u = 2^-11 (one rounding to fp16), S = scale * sum_d |q_d| (|k_d| + r) (r: the
@@ -89,12 +89,17 @@ def attention_ref(q, cache, table, lens, new, scale, causal=True, window=0):
     exp(+-e); p (times a value's scale) and the value round to fp16 once or twice more
     (3 u); the binary32 sums over n keys and their joins add (n + 16) 2^-23.  All of it
     acts on sum_j p_j (|v_j| + r_j), and the normalised sum can move by the same
-    relative amount once more."""
+    relative amount once more.
+    lse_bound: every p_j moves by a factor of at most exp(+-e'), e' the exponent above, so
+    the logarithm of their sum moves by e' at most, and by the sum's binary32 error
+    (n + 16) 2^-23; its own rounding and that of the maximum's scaling add 2^-22 of the
+    largest score and of the result."""
     u = 2.0 ** -11
     T, Hq, D = q.shape
     P, H = cache.page_size, cache.num_heads
     qd = q.detach().double().cpu().numpy()
     out, lse, bound = np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf), np.zeros((T, Hq, D))
+    lse_bound = np.zeros((T, Hq))
     at = 0
     for b, (L, n) in enumerate(zip(lens, new)):
         pages = torch.from_numpy(table[b, : -(-L // P)].astype(np.int64)).to(cache.k_codes.device)
@@ -122,10 +127,13 @@ def attention_ref(q, cache, table, lens, new, scale, causal=True, window=0):
             w = w / np.where(total > 0, total, 1)
             out[at:at + n, hq] = w @ v
             lse[at:at + n, hq][ok] = (m + np.log(np.where(total > 0, total, 1)))[ok, 0]
-            e = np.expm1((2 * u + (D + 8) * 2.0 ** -23) * np.where(seen, big, 0).max(1, initial=0))[:, None]
+            most = np.where(seen, big, 0).max(1, initial=0)
+            e = np.expm1((2 * u + (D + 8) * 2.0 ** -23) * most)[:, None]
+            lse_bound[at:at + n, hq] = ((2 * u + (D + 8) * 2.0 ** -23) * most + (L + 16) * 2.0 ** -23
+                                        + 2.0 ** -22 * (most + np.log(L + 2.0)))
             bound[at:at + n, hq] = (2 * e + 3 * u + (L + 16) * 2.0 ** -22) * (w @ (np.abs(v) + rng[1][h]))
         at += n
-    return out, lse, bound
+    return out, lse, bound, lse_bound
 
 
 def assert_attention(got: torch.Tensor, ref: np.ndarray, bound: np.ndarray, what: str = "") -> None:
