@@ -16,10 +16,10 @@
 // scale and offset enter per token and group in binary32.  p s is rounded to
 // fp16 under a power of two kappa (a shift of the running maximum) that keeps
 // s kappa near 2^4 at p = 1, 2^18 above the first fp16 subnormal.  Codes are
-// taken from their middle (a second product with the constant -8, cheaper than
-// changing the codes) because values have either sign: without it the sum over
-// n keys is large against the result and its truncation shows (0.0013 instead
-// of 0.0003 relative error at 131071 keys).
+// taken from their middle because values have either sign: without it the sum
+// over n keys is large against the result and its truncation shows (0.0013
+// relative error at 131071 keys).  The product does it: half of its depth takes
+// 8 tokens' codes, the other half -8 for the same probabilities.
 //
 // mma.m16n8k16 with keys (16 tokens) or channels (16 of V^T) as its rows and up
 // to 8 query rows as its columns: the accumulators of q.c and of the output
@@ -783,12 +783,14 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
               const uint32_t f0 = e0 >> 8, f1 = e1 >> 8;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma16816(o[nt][g][2 * half], e0 & 0x000F000Fu, f0 & 0x000F000Fu, e1 & 0x000F000Fu, f1 & 0x000F000Fu,
-                         pf[nt][g][0], pf[nt][g][1]);
-                mma16816(o[nt][g][2 * half], kMinus8, kMinus8, kMinus8, kMinus8, pf[nt][g][0], pf[nt][g][1]);
-                mma16816(o[nt][g][2 * half + 1], e0 & 0x00F000F0u, f0 & 0x00F000F0u, e1 & 0x00F000F0u,
-                         f1 & 0x00F000F0u, pf[nt][g][0], pf[nt][g][1]);
-                mma16816(o[nt][g][2 * half + 1], kMinus128, kMinus128, kMinus128, kMinus128, pf[nt][g][0],
+                // the first 8 tokens: their codes, and -8 for the same probabilities; then the others
+                mma16816(o[nt][g][2 * half], e0 & 0x000F000Fu, f0 & 0x000F000Fu, kMinus8, kMinus8, pf[nt][g][0],
+                         pf[nt][g][0]);
+                mma16816(o[nt][g][2 * half], e1 & 0x000F000Fu, f1 & 0x000F000Fu, kMinus8, kMinus8, pf[nt][g][1],
+                         pf[nt][g][1]);
+                mma16816(o[nt][g][2 * half + 1], e0 & 0x00F000F0u, f0 & 0x00F000F0u, kMinus128, kMinus128, pf[nt][g][0],
+                         pf[nt][g][0]);
+                mma16816(o[nt][g][2 * half + 1], e1 & 0x00F000F0u, f1 & 0x00F000F0u, kMinus128, kMinus128, pf[nt][g][1],
                          pf[nt][g][1]);
               }
             }
