@@ -723,6 +723,10 @@ qg_status check_cache(const qg_kv4_cache* c, KV4* out) {
   out->heads = (int)c->num_heads;
   out->page_size = (int)c->page_size;
   out->dim = (int)c->head_dim;
+  const uint64_t k = (uint64_t)c->page_size / 16;
+  out->page_shift = 32;
+  while ((2ull << (out->page_shift - 32)) <= k) ++out->page_shift;
+  out->page_magic = ((1ull << out->page_shift) + k - 1) / k;
   return QG_OK;
 }
 
@@ -863,7 +867,6 @@ qg_status qg_attention_kv4(const void* q, int64_t q_stride_t, int64_t q_stride_h
   a.heads_q = (int)heads_q;
   a.group = (int)heads_q / a.cache.heads;
   a.max_pages = (int)max_pages;
-  a.page_magic = ((1ull << 40) + a.cache.page_size / 16 - 1) / (a.cache.page_size / 16);
   a.scale = scale;
   a.causal = causal != 0;
   a.window = (int)std::min<int64_t>(window, kMaxDim - 1);

@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
     page = -1;
     const int t = (fill.s.c0 + fill.c) * kChunk + pc * piece;
     if (copies && t < fill.s.len) {
-      const int i = (int)(((uint64_t)(uint32_t)(t >> 4) * a.page_magic) >> 40);  // t / P
+      const int i = (int)kv4_page(a.cache, (uint32_t)t >> 4);  // t / P
       in_page = t - i * P;
       page = __ldg(a.table + (int64_t)fill.b * a.table_ld + i);
       if (page < 0 || page >= a.cache.pages) {

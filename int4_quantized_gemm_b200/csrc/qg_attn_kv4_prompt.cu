@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int page = -1, in_page = 0;
       const int t = first_step * kKeys + i * kHalf + pc * piece;
       if (arr < 4 && t < job.len) {
-        const int pi = (int)(((uint64_t)(uint32_t)(t >> 4) * a.page_magic) >> 40);
+        const int pi = (int)kv4_page(a.cache, (uint32_t)t >> 4);
         in_page = t - pi * P;
         page = __ldg(a.table + (int64_t)job.b * a.table_ld + pi);
         if (page < 0 || page >= a.cache.pages) {

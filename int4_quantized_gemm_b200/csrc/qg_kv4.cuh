@@ -24,7 +24,16 @@ struct KV4 {
   uint32_t* params[2];  // fp16 (scale, offset) in one word
   int64_t pages;
   int heads, page_size, dim;
+  // floor(n / (page_size / 16)) = n * magic >> shift for n < 2^31: magic = ceil(2^shift / k), 2^(shift - 32) <= k,
+  // so n * (magic - 2^shift / k) < 2^31 < 2^shift / k and n * magic < 2^64
+  uint64_t page_magic;
+  int page_shift;
 };
+
+// The page of a token position below 2^35 (page_size is a multiple of 16)
+__host__ __device__ __forceinline__ uint32_t kv4_page(const KV4& c, uint32_t sixteenths) {
+  return (uint32_t)(sixteenths * c.page_magic >> c.page_shift);
+}
 
 // First token row of (page, head)
 __host__ __device__ __forceinline__ int64_t kv4_row(const KV4& c, int64_t page, int head) {
@@ -46,7 +55,6 @@ struct Attn4 {
   int n_uniform;
   int B, T, heads_q, group;  // group = heads_q / heads
   int max_pages;
-  uint64_t page_magic;  // (t >> 4) * page_magic >> 40 = t / page_size for t < 2^31 (page_size / 16 <= 4096)
   float scale;
   int causal;
   int window;  // 0: none

@@ -17,6 +17,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 
 #include "qg_device.cuh"
@@ -234,7 +235,7 @@ cudaError_t launch_norm(const void* x, int64_t ldx, const void* residual, int64_
   return go(rmsnorm_quantize_kernel<T, 512, 1, 0>, 512, 1);
 }
 
-// One block row per matrix row (grid-strided), 8 codes per thread and step.
+// 8 codes per thread and step, VEC steps in flight.
 template <typename T>
 __device__ __forceinline__ void store8(T* y, const float (&v)[8]);
 template <>
@@ -254,40 +255,50 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* y, const fl
                  pair_bits<__nv_bfloat16>(v[4], v[5]), pair_bits<__nv_bfloat16>(v[6], v[7]));
 }
 
-template <typename T>
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) dequantize_rowwise_kernel(const int8_t* __restrict__ xq, int64_t ldq,
                                                                  const float* __restrict__ xs, T* __restrict__ y,
                                                                  int64_t ldy, int M, int K) {
   pdl_trigger();
   pdl_wait();
-  const int nvec = K / 8;
-  const int first = blockIdx.y * 256 + threadIdx.x, step = 256 * gridDim.y;
+  const int nvec = K / 8, t = threadIdx.x, first = blockIdx.y * (256 * VEC) + t;
   for (int m = blockIdx.x; m < M; m += gridDim.x) {
-    const float s = __ldg(xs + m);
     const int8_t* q = xq + (int64_t)m * ldq;
     T* out = y + (int64_t)m * ldy;
-    for (int i = first; i < nvec; i += step) {
-      const uint2 c = __ldg(reinterpret_cast<const uint2*>(q) + i);
-      float v[8];
+    const float s = __ldg(xs + m);
+#pragma unroll 1
+    for (int64_t base = first; base < nvec; base += (int64_t)gridDim.y * (256 * VEC)) {
+      uint2 c[VEC];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = __fmul_rn((float)(int8_t)(c.x >> (8 * j)), s);
-        v[4 + j] = __fmul_rn((float)(int8_t)(c.y >> (8 * j)), s);
+      for (int j = 0; j < VEC; ++j)
+        if (base + 256 * j < nvec) c[j] = __ldg(reinterpret_cast<const uint2*>(q) + base + 256 * j);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        if (base + 256 * j >= nvec) break;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = __fmul_rn((float)(int8_t)(c[j].x >> (8 * k)), s);
+          v[4 + k] = __fmul_rn((float)(int8_t)(c[j].y >> (8 * k)), s);
+        }
+        store8<T>(out + 8 * (base + 256 * j), v);
       }
-      store8<T>(out + 8 * i, v);
     }
-    const int kt = nvec * 8 + first;
-    if (kt < K) out[kt] = (T)__fmul_rn((float)q[kt], s);
+    const int kt = nvec * 8 + t;
+    if (blockIdx.y == 0 && kt < K) out[kt] = (T)__fmul_rn((float)q[kt], s);
   }
 }
 
 template <typename T>
 cudaError_t launch_dequant(const int8_t* xq, int64_t ldq, const float* xs, void* y, int64_t ldy, int M, int K,
                            cudaStream_t s) {
-  const unsigned gy = (unsigned)std::max(1, std::min(8, (K / 8 + 255) / 256));
-  LaunchCfg lc((unsigned)std::min<int64_t>(M, (int64_t)sm_count() * 64), 256, 0, s);
-  lc.cfg.gridDim.y = gy;
-  return cudaLaunchKernelEx(&lc.cfg, dequantize_rowwise_kernel<T>, xq, ldq, xs, static_cast<T*>(y), ldy, M, K);
+  auto go = [&](auto kernel, int vec) {
+    const int64_t gy = std::max(1, (K / 8 + 256 * vec - 1) / (256 * vec));
+    LaunchCfg lc((unsigned)std::min<int64_t>(M, ((int64_t)1 << 31) - 1), 256, 0, s);
+    lc.cfg.gridDim.y = (unsigned)std::min<int64_t>(gy, 65535);
+    return cudaLaunchKernelEx(&lc.cfg, kernel, xq, ldq, xs, static_cast<T*>(y), ldy, M, K);
+  };
+  return K <= 2048 ? go(dequantize_rowwise_kernel<T, 1>, 1) : go(dequantize_rowwise_kernel<T, 2>, 2);
 }
 
 }  // namespace
