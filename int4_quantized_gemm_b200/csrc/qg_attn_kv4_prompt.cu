@@ -5,8 +5,9 @@
 // Compute-bound: 4 dim operations and one exponential per (row, key).  One CTA
 // takes 256 rows (two tiles of 128) of a (sequence, KV head) and walks over the
 // keys 128 at a time:
-//   loader warp      packed codes and params of 64 tokens a stage, bulk copies
-//   4 warps          codes -> fp16 (c s + o, one rounding) into the swizzled
+//   2 loader warps   packed codes and params of 64 tokens a stage, bulk copies,
+//                    keys and values in rings of their own
+//   2 x 4 warps      codes -> fp16 (c s + o, one rounding) into the swizzled
 //                    K-major operands K [key][channel] and V^T [channel][key];
 //                    both row tiles share them
 //   MMA warp         tcgen05: S = Q K^T (M 128, N 128, K dim) and O += P V
@@ -53,8 +54,8 @@ constexpr int kRows = 256;      // query rows per CTA, two tiles of 128
 constexpr int kKeys = 128;      // keys per step
 constexpr int kHalf = 64;       // tokens per raw stage
 constexpr int kRaw = 3;         // raw stages
-constexpr int kThreads = 448;
-constexpr int kDequantWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
+constexpr int kThreads = 608;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kLoadWarp = 17;  // loaders: keys, values
 constexpr float kLift = 7.0f, kAhead = 8.0f;
 
 enum : uint32_t {
@@ -103,6 +104,26 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// D = A B and D += A B, one K step; the second with A in tensor memory too.
+__device__ __forceinline__ void mma_first(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_next(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, 1, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_next_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, 1, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -116,11 +137,22 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&c)[4]) {
   c[3] = h2_fma((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
 }
 
-// Is the largest code's value not a finite fp16 (params that are not finite, or a value beyond the type)?
-__device__ __forceinline__ bool odd_params(uint32_t p) {
-  const __half2 so = *reinterpret_cast<__half2*>(&p);
-  const __half top = __hfma(__low2half(so), __float2half(15.0f), __high2half(so));
-  return (__half_as_ushort(top) & 0x7C00u) == 0x7C00u;
+// Does any of a stage's params (words of 4 bytes, for the whole warp to look at) give a value that is not a finite
+// fp16: not finite itself, or its largest code's value beyond the type?
+template <int WORDS>
+__device__ __forceinline__ bool any_odd(const uint8_t* params, int lane) {
+  static_assert(WORDS % 64 == 0, "");
+  uint32_t most = 0;  // the largest magnitudes; NaN if one is
+#pragma unroll
+  for (int i = 0; i < WORDS / 64; ++i) {
+    const uint2 w = *reinterpret_cast<const uint2*>(params + (i * 32 + lane) * 8);
+    const uint32_t top = h2_fma(__byte_perm(w.x, w.y, 0x5410), 0x4B804B80u, __byte_perm(w.x, w.y, 0x7632)) & 0x7FFF7FFFu;
+    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(most) : "r"(top));
+  }
+  return __any_sync(0xffffffffu, (most & 0x7C00u) == 0x7C00u || (most & 0x7C000000u) == 0x7C000000u);
+}
+__device__ __forceinline__ bool not_finite(uint32_t p) {
+  return (p & 0x7C00u) == 0x7C00u || (p & 0x7C000000u) == 0x7C000000u;
 }
 
 struct Job {
@@ -179,11 +211,67 @@ struct Layout {
   static constexpr uint32_t q = 0;                              // [2 tiles]
   static constexpr uint32_t k = 2 * kOperand;                   // [2 buffers] [G][128 keys][64 channels]
   static constexpr uint32_t v = 4 * kOperand;                   // [2 buffers] [2][D rows][64 keys]
-  static constexpr uint32_t raw = 6 * kOperand;                 // [kRaw]
+  // stages of 64 tokens: keys' codes and params and the values' params; values' codes and params
   static constexpr uint32_t kCodes = kHalf * D / 2, kParams = kHalf * G * 4;
-  static constexpr uint32_t kStage = 2 * (kCodes + kParams);
-  static constexpr uint32_t bytes = raw + kRaw * kStage;
+  static constexpr uint32_t kKeyStage = kCodes + 2 * kParams, kValueStage = kCodes + kParams;
+  static constexpr uint32_t keys = 6 * kOperand, values = keys + kRaw * kKeyStage;
+  static constexpr uint32_t bytes = values + kRaw * kValueStage;
 };
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// The largest of a row's 128 scores (kAll: all of them, else columns [cb, ce)).
+template <bool kAll>
+__device__ __forceinline__ float row_max(uint32_t ts, int cb, int ce) {
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t v[2][32];
+    tmem_ld32(ts + 64 * c, v[0]);
+    tmem_ld32(ts + 64 * c + 32, v[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int col = 64 * c + 32 * h + i;
+        if (kAll || (col >= cb && col < ce)) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(v[h][i]));
+      }
+  }
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+// Replaces a row's scores x by p = 2^(x sigma + mneg) in fp16 (over the first 64 of its columns, each behind what has
+// been read) and returns their sum.
+template <bool kAll>
+__device__ __forceinline__ float row_exp(uint32_t ts, float sigma, float mneg, int cb, int ce) {
+  float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  uint32_t v[2][16];
+  tmem_ld16(ts, v[0]);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    tmem_ld_wait();
+    if (c < 7) tmem_ld16(ts + 16 * (c + 1), v[(c + 1) & 1]);  // in flight while these are computed
+    uint32_t p[8];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      float x[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        x[k] = ex2(fmaf(__uint_as_float(v[c & 1][i + k]), sigma, mneg));
+        if (!kAll && (16 * c + i + k < cb || 16 * c + i + k >= ce)) x[k] = 0.0f;
+        part[(i + k) & 3] += x[k];
+      }
+      p[i / 2] = half2_bits(x[0], x[1]);
+    }
+    tmem_st8(ts + 8 * c, p);
+  }
+  return (part[0] + part[1]) + (part[2] + part[3]);
+}
 
 // A part of a row for the join: D sums, then (log2 maximum, sum).
 template <int G>
@@ -198,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Layout<G>;
   constexpr int D = L::D;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2],
+  __shared__ __align__(8) uint64_t raw_full[2][kRaw], raw_empty[2][kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2],
       s_full[2], p_full[2], o_done[2], drained;
   __shared__ uint32_t tmem_slot;
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -206,9 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
 
   if (tid == 0) {
-    for (int i = 0; i < kRaw; ++i) {
-      mbar_init(smem_u32(&raw_full[i]), 1);
-      mbar_init(smem_u32(&raw_empty[i]), 4);
+    for (int i = 0; i < 2 * kRaw; ++i) {
+      mbar_init(smem_u32(&raw_full[0][i]), 1);
+      mbar_init(smem_u32(&raw_empty[0][i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&k_full[i]), 4);
@@ -259,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // --- queries: a thread per row, scaled by a power of two to fp16 -------------
   float sigma = 0.0f;
   const int tile = warp / 4 & 1, row = row0 + tid;  // softmax warps
-  if (warp < kDequantWarp) {
+  if (warp < kKeyWarp) {
     uint4 v[D / 8];
     float amax = 0.0f;
     if (row < job.rows) {
@@ -302,20 +390,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   const uint32_t tm_s = tmem, tm_o = tmem + 256;  // S: 128 columns a tile; O: D columns a tile
 
-  if (warp == kLoadWarp) {
-    // ---- packed codes and params --------------------------------------------
+  if (warp >= kLoadWarp) {
+    // ---- packed codes and params: one warp for the keys' ring, one for the values' ---------
+    const int ring = warp - kLoadWarp;
+    const uint32_t base = sm + (ring ? L::values : L::keys), stage_bytes = ring ? L::kValueStage : L::kKeyStage;
     const int P = a.cache.page_size;
     const int piece = min(kHalf, P & -P), pieces = kHalf / piece;
-    const int arr = lane / pieces, pc = lane % pieces;
-    const uint32_t bytes = arr < 2 ? piece * (D / 2) : piece * (G * 4);
-    const uint32_t dst_off = (arr < 2 ? arr * L::kCodes : 2 * L::kCodes + (arr - 2) * L::kParams) + pc * bytes;
-    const uint32_t code_lanes = (1u << (2 * pieces)) - 1;
+    const int arr = lane / pieces, pc = lane % pieces;  // 0 codes, 1 params, 2 (keys' ring) the values' params
+    const int arrays = ring ? 2 : 3;
+    const uint32_t bytes = arr == 0 ? piece * (D / 2) : piece * (G * 4);
+    const uint32_t dst_off = (arr == 0 ? 0 : L::kCodes + (arr - 1) * L::kParams) + pc * bytes;
+    const uint32_t code_lanes = (1u << pieces) - 1;
+    const uint32_t* src = arr == 0 ? (ring ? a.cache.codes[1] : a.cache.codes[0])
+                                   : (ring || arr == 2 ? a.cache.params[1] : a.cache.params[0]);
     int issued = 0;
 #pragma unroll 1
     for (int i = 0; i < 2 * total; ++i) {
       int page = -1, in_page = 0;
       const int t = first_step * kKeys + i * kHalf + pc * piece;
-      if (arr < 4 && t < job.len) {
+      if (arr < arrays && t < job.len) {
         const int pi = (int)kv4_page(a.cache, (uint32_t)t >> 4);
         in_page = t - pi * P;
         page = __ldg(a.table + (int64_t)job.b * a.table_ld + pi);
@@ -325,45 +418,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const int st = i % kRaw;
-      if (!mbar_wait(smem_u32(&raw_empty[st]), (i / kRaw & 1) ^ 1, &g_status_prompt, kSiteRawEmpty)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&raw_empty[ring][st]), (i / kRaw & 1) ^ 1, &g_status_prompt, kSiteRawEmpty))) break;
       const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-      const uint32_t bar = smem_u32(&raw_full[st]);
+      const uint32_t bar = smem_u32(&raw_full[ring][st]);
       if (lane == 0)
         mbar_arrive_expect_tx(bar, __popc(have & code_lanes) * (uint32_t)(piece * (D / 2)) +
                                        __popc(have & ~code_lanes) * (uint32_t)(piece * (G * 4)));
       __syncwarp();
       if (page >= 0) {
         const int64_t r = kv4_row(a.cache, page, job.h) + in_page;
-        const uint32_t* src = arr < 2 ? (arr == 0 ? a.cache.codes[0] : a.cache.codes[1]) + r * (D / 8)
-                                      : (arr == 2 ? a.cache.params[0] : a.cache.params[1]) + r * G;
-        bulk_load(sm + L::raw + st * L::kStage + dst_off, src, bytes, bar);
+        bulk_load(base + st * stage_bytes + dst_off, src + r * (arr == 0 ? D / 8 : G), bytes, bar);
       }
       issued = i + 1;
     }
     // no copy in flight outlives the CTA
     for (int i = max(0, issued - kRaw); i < issued; ++i)
-      mbar_wait(smem_u32(&raw_full[i % kRaw]), i / kRaw & 1, &g_status_prompt, kSiteDrain);
+      mbar_wait(smem_u32(&raw_full[ring][i % kRaw]), i / kRaw & 1, &g_status_prompt, kSiteDrain);
   } else if (warp == kMmaWarp) {
     // ---- tensor cores ---------------------------------------------------------
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys), kIdescO = idesc_f16_f32(128, D);
+      // descriptors of the operands' first blocks; a step along K or a block further only adds to the address field
+      const uint64_t dq = sdesc_sw128(sm + L::q), dk = sdesc_sw128(sm + L::k), dv = sdesc_sw128(sm + L::v);
       const auto scores = [&](int t, int buf) {
+        const uint64_t q = dq + (uint32_t)t * (L::kOperand >> 4), k = dk + (uint32_t)buf * (L::kOperand >> 4);
+        const uint32_t d = tm_s + t * 128;
+        mma_first(d, q, k, kIdescS);
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16(tm_s + t * 128, sdesc_sw128(sm + L::q + t * L::kOperand + g * L::kBlock + k * 32),
-                    sdesc_sw128(sm + L::k + buf * L::kOperand + g * L::kBlock + k * 32), kIdescS, (g | k) != 0);
+        for (int i = 1; i < 4 * G; ++i)
+          mma_next(d, q + (uint32_t)((i / 4 * L::kBlock + i % 4 * 32) >> 4), k + (uint32_t)((i / 4 * L::kBlock + i % 4 * 32) >> 4),
+                   kIdescS);
         mma_commit(smem_u32(&s_full[t]));
       };
       const auto outputs = [&](int t, int buf, bool more) {
+        const uint64_t v = dv + (uint32_t)buf * (L::kOperand >> 4);
+        const uint32_t d = tm_o + t * D, p = tm_s + t * 128;
+        mma_f16_ts(d, p, v, kIdescO, more);
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ts(tm_o + t * D, tm_s + t * 128 + b * 32 + k * 8,
-                       sdesc_sw128(sm + L::v + buf * L::kOperand + b * (D * 128) + k * 32), kIdescO,
-                       more || (b | k) != 0);
+        for (int i = 1; i < 8; ++i)
+          mma_next_ts(d, p + i * 8, v + (uint32_t)((i / 4 * (D * 128) + i % 4 * 32) >> 4), kIdescO);
         mma_commit(smem_u32(&o_done[t]));
       };
       const auto wait = [&](uint64_t& bar, int parity, uint32_t site) {
@@ -384,15 +477,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < total && ok; ++j) {
         const int buf = j & 1, par = j >> 1 & 1;
         ok = wait(v_full[buf], par, kSiteVFull);
-        if (ok && j + 1 < total) ok = wait(k_full[buf ^ 1], (j + 1) >> 1 & 1, kSiteKFull);
+        bool keys = false;  // the next step's have come
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (ok && j < steps[t]) {
             ok = wait(p_full[t], j & 1, kSiteP);
             if (!ok) break;
             outputs(t, buf, j > 0);
-            // in order behind the product that reads P from the same columns
-            if (j + 1 < steps[t]) scores(t, buf ^ 1);
+            if (j + 1 < steps[t]) {
+              if (!keys) ok = wait(k_full[buf ^ 1], (j + 1) >> 1 & 1, kSiteKFull);
+              if (!ok) break;
+              keys = true;
+              scores(t, buf ^ 1);  // in order behind the product that reads P from the same columns
+            }
           }
         mma_commit(smem_u32(&v_empty[buf]));
         if (j + 1 < total) mma_commit(smem_u32(&k_empty[buf ^ 1]));
@@ -401,96 +498,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(smem_u32(&drained), 0, &g_status_prompt, kSiteDrain);
     }
     __syncwarp();
-  } else if (warp >= kDequantWarp) {
-    // ---- codes to fp16 ----------------------------------------------------------
-    const int dt = tid - 32 * kDequantWarp;
-    bool ok = true;
+  } else if (warp >= kValueWarp) {
+    // ---- values to fp16: a lane takes one word (8 channels) of 8 tokens and writes 8 tokens of 8 channels ----
+    const int dt = tid - 32 * kValueWarp;
+    const int jw = dt & 7, g = G == 2 ? dt >> 3 & 1 : 0, tg = dt >> (G == 2 ? 4 : 3);
+    const int swap = tg & 1;  // odd groups read their pairs the other way round: no bank twice
+    const uint32_t sel_lo = swap ? 0x1054u : 0x5410u, sel_hi = swap ? 0x3276u : 0x7632u;
 #pragma unroll 1
-    for (int i = 0; i < 2 * total && ok; ++i) {
+    for (int i = 0; i < 2 * total; ++i) {
       const int j = i >> 1, half = i & 1, buf = j & 1, st = i % kRaw;
-      if (half == 0) {
-        ok = mbar_wait(smem_u32(&k_empty[buf]), (j >> 1 & 1) ^ 1, &g_status_prompt, kSiteKEmpty) &&
-             mbar_wait(smem_u32(&v_empty[buf]), (j >> 1 & 1) ^ 1, &g_status_prompt, kSiteVEmpty);
-        if (!ok) break;
-      }
-      ok = mbar_wait(smem_u32(&raw_full[st]), i / kRaw & 1, &g_status_prompt, kSiteRawFull);
-      if (!ok) break;
-      const uint8_t* raw = smp + L::raw + st * L::kStage;
-      const uint8_t *kc = raw, *vc = raw + L::kCodes, *kp = raw + 2 * L::kCodes, *vp = kp + L::kParams;
+      bool ok = true;
+      if (half == 0) ok = mbar_wait(smem_u32(&v_empty[buf]), (j >> 1 & 1) ^ 1, &g_status_prompt, kSiteVEmpty);
+      if (ok) ok = mbar_wait(smem_u32(&raw_full[1][st]), i / kRaw & 1, &g_status_prompt, kSiteRawFull);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t* vc = smp + L::values + st * L::kValueStage;
+      const uint8_t* vp = vc + L::kCodes;
       const int t0 = (first_step + j) * kKeys + half * kHalf;
-
-      // keys: a lane takes 4 words (32 channels) of one token
-      constexpr int kParts = D / 32;  // lanes per token
-#pragma unroll
-      for (int it = 0; it < kParts / 2; ++it) {
-        const int item = dt + 128 * it, part = item % kParts, tok = item / kParts;
-        // the warp's tokens: is any value of theirs not an fp16?
-        uint32_t kpw[G], vpw[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          kpw[g] = *reinterpret_cast<const uint32_t*>(kp + (tok * G + g) * 4);
-          vpw[g] = *reinterpret_cast<const uint32_t*>(vp + (tok * G + g) * 4);
-        }
-        bool odd = false;
-#pragma unroll
-        for (int g = 0; g < G; ++g) odd |= odd_params(kpw[g]) | odd_params(vpw[g]);
-        const uint4 words = *reinterpret_cast<const uint4*>(kc + tok * (D / 2) + part * 16);
-        const uint32_t* w = &words.x;
-        uint32_t out[4][4];
-        uint32_t s2[G], o2[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          s2[g] = __byte_perm(kpw[g], 0, 0x1010);
-          o2[g] = __byte_perm(kpw[g], 0, 0x3232);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t c[4];
-          codes_f16(w[k], c);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) out[k][m] = h2_fma(c[m], s2[k % G], o2[k % G]);
-        }
-        if (__any_sync(0xffffffffu, odd)) {
-          // A value that is not finite makes the key NaN: every row that sees the token becomes NaN, none else
-          // (the value itself is taken finite below).  Large keys are held to the type.
-          bool bad = false;
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-            bad |= (vpw[g] & 0x7C00u) == 0x7C00u || (vpw[g] & 0x7C000000u) == 0x7C000000u ||
-                   (kpw[g] & 0x7C00u) == 0x7C00u || (kpw[g] & 0x7C000000u) == 0x7C000000u;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) out[k][m] = bad ? 0x7FFF7FFFu : h2_finite(out[k][m]);
-        }
-        // word k of the lane is word [j, g] of the token: index part * 4 + k = j G + g
-        const uint32_t krow = sm + L::k + buf * L::kOperand + (half * kHalf + tok) * 128;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int jw = (part * 4 + k) / G;
-          sts128(krow + (k % G) * L::kBlock + ((jw ^ (tok & 7)) << 4), out[k][0], out[k][1], out[k][2], out[k][3]);
-        }
-      }
-      if (half == 1) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&k_full[buf]));
-      }
-
-      // values: a lane takes one word (8 channels) of 8 tokens and writes 8 tokens of 8 channels
+      const bool odd = any_odd<kHalf * G>(vp, lane) || t0 < lo || t0 + kHalf > job.len;
       if (G == 2 || dt < 64) {
-        const int jw = dt & 7, g = G == 2 ? dt >> 3 & 1 : 0, tg = dt >> (G == 2 ? 4 : 3);
-        const int swap = tg & 1;  // odd groups read their pairs the other way round: no bank twice
         uint32_t pw[8];
-        bool odd = false;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          pw[k] = *reinterpret_cast<const uint32_t*>(vp + ((tg * 8 + k) * G + g) * 4);
-          const int t = t0 + tg * 8 + k;
-          odd |= odd_params(pw[k]) || t < lo || t >= job.len;
-        }
-        const bool any = __any_sync(G == 2 ? 0xffffffffu : 0xffffffffu, odd);
-        if (any) {  // tokens that no row sees: zero
+        for (int k = 0; k < 8; ++k) pw[k] = *reinterpret_cast<const uint32_t*>(vp + ((tg * 8 + k) * G + g) * 4);
+        if (odd) {  // tokens that no row sees: zero
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int t = t0 + tg * 8 + k;
@@ -508,12 +537,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {  // nibbles 0..3, 4..7
             uint32_t c[4];
-            codes_f16(__byte_perm(x, y, hh ? (swap ? 0x3276u : 0x7632u) : (swap ? 0x1054u : 0x5410u)), c);
+            codes_f16(__byte_perm(x, y, hh ? sel_hi : sel_lo), c);
 #pragma unroll
             for (int m = 0; m < 4; ++m) out[4 * hh + m][p] = h2_fma(c[m], s2, o2);
           }
         }
-        if (any) {
+        if (odd) {  // finite (hidden tokens meet p = 0); a visible token's NaN comes through its key
 #pragma unroll
           for (int c = 0; c < 8; ++c)
 #pragma unroll
@@ -524,14 +553,73 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i2 = 0; i2 < 8; ++i2) sts128(vrow + i2 * 8 * 128, out[i2][0], out[i2][1], out[i2][2], out[i2][3]);
       }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&raw_empty[st]));
-      if (half == 1) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&v_full[buf]));
-      } else {
-        fence_proxy_async_smem();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&raw_empty[1][st]));
+        if (half == 1) mbar_arrive(smem_u32(&v_full[buf]));
+      }
+    }
+  } else if (warp >= kKeyWarp) {
+    // ---- keys to fp16: a lane takes 4 words (32 channels) of a token ----------------------------
+    const int dt = tid - 32 * kKeyWarp;
+    constexpr int kParts = D / 32;  // lanes per token
+#pragma unroll 1
+    for (int i = 0; i < 2 * total; ++i) {
+      const int j = i >> 1, half = i & 1, buf = j & 1, st = i % kRaw;
+      bool ok = true;
+      if (half == 0) ok = mbar_wait(smem_u32(&k_empty[buf]), (j >> 1 & 1) ^ 1, &g_status_prompt, kSiteKEmpty);
+      if (ok) ok = mbar_wait(smem_u32(&raw_full[0][st]), i / kRaw & 1, &g_status_prompt, kSiteRawFull);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t* kc = smp + L::keys + st * L::kKeyStage;
+      const uint8_t *kp = kc + L::kCodes, *vp = kp + L::kParams;
+      const bool odd = any_odd<2 * kHalf * G>(kp, lane);  // the values' params lie behind the keys'
+#pragma unroll
+      for (int it = 0; it < kParts / 2; ++it) {
+        const int item = dt + 128 * it, part = item % kParts, tok = item / kParts;
+        uint32_t kpw[G], out[4][4];
+#pragma unroll
+        for (int g = 0; g < G; ++g) kpw[g] = *reinterpret_cast<const uint32_t*>(kp + (tok * G + g) * 4);
+        const uint4 words = *reinterpret_cast<const uint4*>(kc + tok * (D / 2) + part * 16);
+        const uint32_t* w = &words.x;
+        uint32_t s2[G], o2[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          s2[g] = __byte_perm(kpw[g], 0, 0x1010);
+          o2[g] = __byte_perm(kpw[g], 0, 0x3232);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t c[4];
+          codes_f16(w[k], c);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) out[k][m] = h2_fma(c[m], s2[k % G], o2[k % G]);
+        }
+        if (odd) {
+          // A token with params that are not finite gets a NaN key: every row that sees it becomes NaN, none else
+          // (its value is taken finite).  Large keys are held to the type.
+          bool bad = false;
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            bad |= not_finite(kpw[g]) || not_finite(*reinterpret_cast<const uint32_t*>(vp + (tok * G + g) * 4));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) out[k][m] = bad ? 0x7FFF7FFFu : h2_finite(out[k][m]);
+        }
+        // word k of the lane is word [j, g] of the token: index part * 4 + k = j G + g
+        const uint32_t krow = sm + L::k + buf * L::kOperand + (half * kHalf + tok) * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int jw = (part * 4 + k) / G;
+          sts128(krow + (k % G) * L::kBlock + ((jw ^ (tok & 7)) << 4), out[k][0], out[k][1], out[k][2], out[k][3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&raw_empty[0][st]));
+        if (half == 1) mbar_arrive(smem_u32(&k_full[buf]));
       }
     }
   } else {
@@ -553,21 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t0 = (first_step + j) * kKeys;
       const bool full = t0 >= max_beg && t0 + kKeys <= min_end;
       const int cb = beg - t0, ce = end - t0;  // the visible columns [cb, ce)
-      float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        tmem_ld32(ts + 32 * c, v);
-        tmem_ld_wait();
-        if (full) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= cb && 32 * c + i < ce) top = fmaxf(top, __uint_as_float(v[i]));
-        }
-      }
+      const float top = full ? row_max<true>(ts, cb, ce) : row_max<false>(ts, cb, ce);
       const bool far = top > -INFINITY && (m == -INFINITY || (top - m) * sigma > kAhead);
       if (__any_sync(0xffffffffu, far)) {
         const float mn = fmaxf(m, top);
@@ -590,24 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32], p[16];
-        tmem_ld32(ts + 32 * c, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float x = ex2(fmaf(__uint_as_float(v[i]), sigma, mneg));
-          if (!full && (32 * c + i < cb || 32 * c + i >= ce)) x = 0.0f;
-          part[i & 3] += x;
-          v[i] = __float_as_uint(x);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = half2_bits(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-        tmem_st16(ts + 16 * c, p);  // over columns that have been read
-      }
-      l += (part[0] + part[1]) + (part[2] + part[3]);
+      l += full ? row_exp<true>(ts, sigma, mneg, cb, ce) : row_exp<false>(ts, sigma, mneg, cb, ce);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(smem_u32(&p_full[tile]));
