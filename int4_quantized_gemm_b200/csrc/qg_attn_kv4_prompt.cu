@@ -54,8 +54,9 @@ constexpr int kRows = 256;      // query rows per CTA, two tiles of 128
 constexpr int kKeys = 128;      // keys per step
 constexpr int kHalf = 64;       // tokens per raw stage
 constexpr int kRaw = 3;         // raw stages
-constexpr int kThreads = 608;
-constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kLoadWarp = 17;  // loaders: keys, values
+constexpr int kThreads = 640;
+// Warp 3 does nothing (softmax warp w reads tensor-memory lanes 32 (w % 4) ..).
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kSoftmaxWarp = 4, kKeyWarp = 12, kValueWarp = 16;  // loaders: keys, values
 constexpr float kLift = 7.0f, kAhead = 8.0f;
 
 enum : uint32_t {
@@ -102,6 +103,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
       "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// True on one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // D = A B and D += A B, one K step; the second with A in tensor memory too.
@@ -346,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // --- queries: a thread per row, scaled by a power of two to fp16 -------------
   float sigma = 0.0f;
-  const int tile = warp / 4 & 1, row = row0 + tid;  // softmax warps
-  if (warp < kKeyWarp) {
+  const int tile = (warp - kSoftmaxWarp) / 4 & 1, st_row = tid - 32 * kSoftmaxWarp, row = row0 + st_row;  // softmax warps
+  if (warp >= kSoftmaxWarp && warp < kKeyWarp) {
     uint4 v[D / 8];
     float amax = 0.0f;
     if (row < job.rows) {
@@ -375,11 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     e = max(-100, min(100, e));
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
     sigma = a.scale * 1.44269504088896f * __uint_as_float((uint32_t)(127 - e) << 23);
-    const uint32_t qrow = sm + L::q + tile * L::kOperand + (tid & 127) * 128;
+    const uint32_t qrow = sm + L::q + tile * L::kOperand + (st_row & 127) * 128;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
       const float2 f0 = values(v[i].x), f1 = values(v[i].y), f2 = values(v[i].z), f3 = values(v[i].w);
-      sts128(qrow + (i / 8) * L::kBlock + (((i & 7) ^ (tid & 7)) << 4), half2_bits(f0.x * up, f2.x * up),
+      sts128(qrow + (i / 8) * L::kBlock + (((i & 7) ^ (st_row & 7)) << 4), half2_bits(f0.x * up, f2.x * up),
              half2_bits(f0.y * up, f2.y * up), half2_bits(f1.x * up, f3.x * up), half2_bits(f1.y * up, f3.y * up));
     }
     fence_proxy_async_smem();
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   const uint32_t tm_s = tmem, tm_o = tmem + 256;  // S: 128 columns a tile; O: D columns a tile
 
-  if (warp >= kLoadWarp) {
+  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
     // ---- packed codes and params: one warp for the keys' ring, one for the values' ---------
     const int ring = warp - kLoadWarp;
     const uint32_t base = sm + (ring ? L::values : L::keys), stage_bytes = ring ? L::kValueStage : L::kKeyStage;
@@ -436,67 +444,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(smem_u32(&raw_full[ring][i % kRaw]), i / kRaw & 1, &g_status_prompt, kSiteDrain);
   } else if (warp == kMmaWarp) {
     // ---- tensor cores ---------------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys), kIdescO = idesc_f16_f32(128, D);
-      // descriptors of the operands' first blocks; a step along K or a block further only adds to the address field
-      const uint64_t dq = sdesc_sw128(sm + L::q), dk = sdesc_sw128(sm + L::k), dv = sdesc_sw128(sm + L::v);
-      const auto scores = [&](int t, int buf) {
-        const uint64_t q = dq + (uint32_t)t * (L::kOperand >> 4), k = dk + (uint32_t)buf * (L::kOperand >> 4);
-        const uint32_t d = tm_s + t * 128;
+    // The whole warp runs this with warp-uniform operands and one elected lane issues: from a branch of one lane the
+    // operands go through vector registers and an MMA costs 175 cycles instead of 65.
+    constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys), kIdescO = idesc_f16_f32(128, D);
+    // descriptors of the operands' first blocks; a step along K or a block further only adds to the address field
+    const uint64_t dq = sdesc_sw128(sm + L::q), dk = sdesc_sw128(sm + L::k), dv = sdesc_sw128(sm + L::v);
+    const uint32_t um_s = __shfl_sync(0xffffffffu, tm_s, 0), um_o = __shfl_sync(0xffffffffu, tm_o, 0);
+    const auto scores = [&](int t, int buf) {
+      const uint64_t q = dq + (uint32_t)t * (L::kOperand >> 4), k = dk + (uint32_t)buf * (L::kOperand >> 4);
+      const uint32_t d = um_s + t * 128;
+      if (elect_one()) {
         mma_first(d, q, k, kIdescS);
 #pragma unroll
         for (int i = 1; i < 4 * G; ++i)
           mma_next(d, q + (uint32_t)((i / 4 * L::kBlock + i % 4 * 32) >> 4), k + (uint32_t)((i / 4 * L::kBlock + i % 4 * 32) >> 4),
                    kIdescS);
         mma_commit(smem_u32(&s_full[t]));
-      };
-      const auto outputs = [&](int t, int buf, bool more) {
-        const uint64_t v = dv + (uint32_t)buf * (L::kOperand >> 4);
-        const uint32_t d = tm_o + t * D, p = tm_s + t * 128;
+      }
+      __syncwarp();
+    };
+    const auto outputs = [&](int t, int buf, bool more) {
+      const uint64_t v = dv + (uint32_t)buf * (L::kOperand >> 4);
+      const uint32_t d = um_o + t * D, p = um_s + t * 128;
+      if (elect_one()) {
         mma_f16_ts(d, p, v, kIdescO, more);
 #pragma unroll
         for (int i = 1; i < 8; ++i)
           mma_next_ts(d, p + i * 8, v + (uint32_t)((i / 4 * (D * 128) + i % 4 * 32) >> 4), kIdescO);
         mma_commit(smem_u32(&o_done[t]));
-      };
-      const auto wait = [&](uint64_t& bar, int parity, uint32_t site) {
-        const bool ok = mbar_wait(smem_u32(&bar), parity, &g_status_prompt, site);
-        tc_fence_after();
-        return ok;
-      };
-      bool ok = true;
-      if (total > 0) {
-        ok = wait(k_full[0], 0, kSiteKFull);
-        if (ok) {
-          for (int t = 0; t < 2; ++t)
-            if (steps[t] > 0) scores(t, 0);
-          mma_commit(smem_u32(&k_empty[0]));
-        }
       }
-#pragma unroll 1
-      for (int j = 0; j < total && ok; ++j) {
-        const int buf = j & 1, par = j >> 1 & 1;
-        ok = wait(v_full[buf], par, kSiteVFull);
-        bool keys = false;  // the next step's have come
+      __syncwarp();
+    };
+    const auto commit = [&](uint64_t& bar) {
+      if (elect_one()) mma_commit(smem_u32(&bar));
+      __syncwarp();
+    };
+    const auto wait = [&](uint64_t& bar, int parity, uint32_t site) {
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &g_status_prompt, site));
+      tc_fence_after();
+      return ok;
+    };
+    bool ok = total == 0 || wait(k_full[0], 0, kSiteKFull);
+    if (ok && total > 0) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (ok && j < steps[t]) {
-            ok = wait(p_full[t], j & 1, kSiteP);
-            if (!ok) break;
-            outputs(t, buf, j > 0);
-            if (j + 1 < steps[t]) {
-              if (!keys) ok = wait(k_full[buf ^ 1], (j + 1) >> 1 & 1, kSiteKFull);
-              if (!ok) break;
-              keys = true;
-              scores(t, buf ^ 1);  // in order behind the product that reads P from the same columns
-            }
-          }
-        mma_commit(smem_u32(&v_empty[buf]));
-        if (j + 1 < total) mma_commit(smem_u32(&k_empty[buf ^ 1]));
-      }
-      mma_commit(smem_u32(&drained));
-      mbar_wait(smem_u32(&drained), 0, &g_status_prompt, kSiteDrain);
+      for (int t = 0; t < 2; ++t)
+        if (steps[t] > 0) scores(t, 0);
+      commit(k_empty[0]);
     }
+#pragma unroll 1
+    for (int j = 0; j < total && ok; ++j) {
+      const int buf = j & 1, par = j >> 1 & 1;
+      ok = wait(v_full[buf], par, kSiteVFull);
+      bool keys = false;  // the next step's have come
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (ok && j < steps[t]) {
+          ok = wait(p_full[t], j & 1, kSiteP);
+          if (!ok) break;
+          outputs(t, buf, j > 0);
+          if (j + 1 < steps[t]) {
+            if (!keys) ok = wait(k_full[buf ^ 1], (j + 1) >> 1 & 1, kSiteKFull);
+            if (!ok) break;
+            keys = true;
+            scores(t, buf ^ 1);  // in order behind the product that reads P from the same columns
+          }
+        }
+      commit(v_empty[buf]);
+      if (j + 1 < total) commit(k_empty[buf ^ 1]);
+    }
+    commit(drained);
+    mbar_wait(smem_u32(&drained), 0, &g_status_prompt, kSiteDrain);
     __syncwarp();
   } else if (warp >= kValueWarp) {
     // ---- values to fp16: a lane takes one word (8 channels) of 8 tokens and writes 8 tokens of 8 channels ----
@@ -622,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (half == 1) mbar_arrive(smem_u32(&k_full[buf]));
       }
     }
-  } else {
+  } else if (warp >= kSoftmaxWarp) {
     // ---- softmax, one thread per row ------------------------------------------
     const int mine = steps[tile];
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor-memory lane 32 (warp % 4)
