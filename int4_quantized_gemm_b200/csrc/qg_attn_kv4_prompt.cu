@@ -4,18 +4,19 @@
 //
 // Compute-bound: 4 dim operations and one exponential per (row, key).  One CTA
 // takes 256 rows (two tiles of 128) of a (sequence, KV head) and walks over the
-// keys 128 at a time:
+// keys 64 at a time:
 //   2 loader warps   packed codes and params of 64 tokens a stage, bulk copies,
 //                    keys and values in rings of their own
 //   2 x 4 warps      codes -> fp16 (c s + o, one rounding) into the swizzled
 //                    K-major operands K [key][channel] and V^T [channel][key];
 //                    both row tiles share them
-//   MMA warp         tcgen05: S = Q K^T (M 128, N 128, K dim) and O += P V
+//   MMA warp         tcgen05: S = Q K^T (M 128, N 64, K dim) and O += P V
 //                    (P from tensor memory, N dim), accumulators in tensor memory
 //   2 x 4 warps      softmax of a row tile, a thread per row: maximum, p =
 //                    2^(x - m), P in fp16 over S's columns
-// While the tensor cores work for one row tile, the other's softmax runs.  The
-// maximum that scores are taken against moves only when a row passes it by 8
+// Scores of a row tile alternate between two places in tensor memory and run
+// two steps ahead, so its softmax never waits for the products of its own
+// probabilities.  The maximum that scores are taken against moves only when a row passes it by 8
 // binary digits, so the accumulator is rarely rescaled; p carries a factor 2^7
 // that keeps small ones out of fp16's subnormals (p 2^7 < 2^15).
 //
@@ -51,12 +52,13 @@ unsigned long long read_clear_status_prompt(cudaStream_t s) {
 namespace {
 
 constexpr int kRows = 256;      // query rows per CTA, two tiles of 128
-constexpr int kKeys = 128;      // keys per step
-constexpr int kHalf = 64;       // tokens per raw stage
+constexpr int kKeys = 64;       // keys per step
+constexpr int kBuf = 4;         // buffers of dequantized keys and values
 constexpr int kRaw = 3;         // raw stages
 constexpr int kThreads = 640;
-// Warp 3 does nothing (softmax warp w reads tensor-memory lanes 32 (w % 4) ..).
-constexpr int kMmaWarp = 0, kLoadWarp = 1, kSoftmaxWarp = 4, kKeyWarp = 12, kValueWarp = 16;  // loaders: keys, values
+// Warps 0 and 1 issue the products of a row tile each, 2 and 3 load keys and values.  (One warp for both tiles spent
+// half of its time between the products, in waits whose barriers had long completed.)
+constexpr int kMmaWarp = 0, kLoadWarp = 2, kSoftmaxWarp = 4, kKeyWarp = 12, kValueWarp = 16;
 constexpr float kLift = 7.0f, kAhead = 8.0f;
 
 enum : uint32_t {
@@ -216,67 +218,59 @@ struct Layout {
   static constexpr int D = 64 * G;
   static constexpr uint32_t kBlock = 128 * 128;                 // 128 rows of 128 bytes
   static constexpr uint32_t kOperand = G * kBlock;              // 128 x D fp16
-  static constexpr uint32_t q = 0;                              // [2 tiles]
-  static constexpr uint32_t k = 2 * kOperand;                   // [2 buffers] [G][128 keys][64 channels]
-  static constexpr uint32_t v = 4 * kOperand;                   // [2 buffers] [2][D rows][64 keys]
+  static constexpr uint32_t kStep = kKeys * D * 2;              // a step's keys or values
+  static constexpr uint32_t q = 0;                              // [2 tiles] [G][128 rows][64 channels]
+  static constexpr uint32_t k = 2 * kOperand;                   // [kBuf] [G][64 keys][64 channels]
+  static constexpr uint32_t v = k + kBuf * kStep;               // [kBuf] [D rows][64 keys]
   // stages of 64 tokens: keys' codes and params and the values' params; values' codes and params
-  static constexpr uint32_t kCodes = kHalf * D / 2, kParams = kHalf * G * 4;
+  static constexpr uint32_t kCodes = kKeys * D / 2, kParams = kKeys * G * 4;
   static constexpr uint32_t kKeyStage = kCodes + 2 * kParams, kValueStage = kCodes + kParams;
-  static constexpr uint32_t keys = 6 * kOperand, values = keys + kRaw * kKeyStage;
+  static constexpr uint32_t keys = v + kBuf * kStep, values = keys + kRaw * kKeyStage;
   static constexpr uint32_t bytes = values + kRaw * kValueStage;
 };
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
-// The largest of a row's 128 scores (kAll: all of them, else columns [cb, ce)).
+// The largest of a row's 64 scores (kAll: all of them, else columns [cb, ce)).
 template <bool kAll>
-__device__ __forceinline__ float row_max(uint32_t ts, int cb, int ce) {
+__device__ __forceinline__ float row_max(const uint32_t (&v)[2][32], int cb, int ce) {
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t v[2][32];
-    tmem_ld32(ts + 64 * c, v[0]);
-    tmem_ld32(ts + 64 * c + 32, v[1]);
-    tmem_ld_wait();
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int col = 64 * c + 32 * h + i;
-        if (kAll || (col >= cb && col < ce)) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(v[h][i]));
+    for (int i = 0; i < 32; i += 2) {
+      const int col = 32 * c + i;
+      float& t = top[i / 2 & 3];
+      const float x = __uint_as_float(v[c][i]), y = __uint_as_float(v[c][i + 1]);
+      if constexpr (kAll) {
+        t = fmaxf(fmaxf(t, x), y);
+      } else {
+        if (col >= cb && col < ce) t = fmaxf(t, x);
+        if (col + 1 >= cb && col + 1 < ce) t = fmaxf(t, y);
       }
-  }
+    }
   return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
 
-// Replaces a row's scores x by p = 2^(x sigma + mneg) in fp16 (over the first 64 of its columns, each behind what has
-// been read) and returns their sum.
+// Stores p = 2^(x sigma + mneg) of a row's scores x in fp16 over the first half of their columns; returns their sum.
 template <bool kAll>
-__device__ __forceinline__ float row_exp(uint32_t ts, float sigma, float mneg, int cb, int ce) {
+__device__ __forceinline__ float row_exp(const uint32_t (&v)[2][32], uint32_t ts, float sigma, float mneg, int cb, int ce) {
   float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  uint32_t v[2][16];
-  tmem_ld16(ts, v[0]);
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    tmem_ld_wait();
-    if (c < 7) tmem_ld16(ts + 16 * (c + 1), v[(c + 1) & 1]);  // in flight while these are computed
-    uint32_t p[8];
+  for (int c = 0; c < 2; ++c) {
+    uint32_t p[16];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      float x[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        x[k] = ex2(fmaf(__uint_as_float(v[c & 1][i + k]), sigma, mneg));
-        if (!kAll && (16 * c + i + k < cb || 16 * c + i + k >= ce)) x[k] = 0.0f;
-        part[(i + k) & 3] += x[k];
+    for (int i = 0; i < 16; ++i) {
+      float x = ex2(fmaf(__uint_as_float(v[c][2 * i]), sigma, mneg));
+      float y = ex2(fmaf(__uint_as_float(v[c][2 * i + 1]), sigma, mneg));
+      if constexpr (!kAll) {
+        const int col = 32 * c + 2 * i;
+        if (col < cb || col >= ce) x = 0.0f;
+        if (col + 1 < cb || col + 1 >= ce) y = 0.0f;
       }
-      p[i / 2] = half2_bits(x[0], x[1]);
+      part[2 * (i & 1)] += x;
+      part[2 * (i & 1) + 1] += y;
+      p[i] = half2_bits(x, y);
     }
-    tmem_st8(ts + 8 * c, p);
+    tmem_st16(ts + 16 * c, p);
   }
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
@@ -294,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Layout<G>;
   constexpr int D = L::D;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[2][kRaw], raw_empty[2][kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2],
-      s_full[2], p_full[2], o_done[2], drained;
+  __shared__ __align__(8) uint64_t raw_full[2][kRaw], raw_empty[2][kRaw], k_full[kBuf], k_empty[kBuf],
+      v_full[kBuf], v_empty[kBuf], s_full[2][2], p_full[2][2], o_done[2][2], drained;
   __shared__ uint32_t tmem_slot;
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smp = smem_raw + (sm - smem_u32(smem_raw));
@@ -306,16 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&raw_full[0][i]), 1);
       mbar_init(smem_u32(&raw_empty[0][i]), 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBuf; ++i) {
       mbar_init(smem_u32(&k_full[i]), 4);
-      mbar_init(smem_u32(&k_empty[i]), 1);
+      mbar_init(smem_u32(&k_empty[i]), 2);
       mbar_init(smem_u32(&v_full[i]), 4);
-      mbar_init(smem_u32(&v_empty[i]), 1);
-      mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 128);
-      mbar_init(smem_u32(&o_done[i]), 1);
+      mbar_init(smem_u32(&v_empty[i]), 2);
+      mbar_init(smem_u32(&s_full[0][i]), 1);
+      mbar_init(smem_u32(&p_full[0][i]), 128);
+      mbar_init(smem_u32(&o_done[0][i]), 1);
     }
-    mbar_init(smem_u32(&drained), 1);
+    mbar_init(smem_u32(&drained), 2);
     fence_mbar_init();
   }
   pdl_trigger();
@@ -396,14 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   cta_barrier_all();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const uint32_t tm_s = tmem, tm_o = tmem + 256;  // S: 128 columns a tile; O: D columns a tile
+  const uint32_t tm_s = tmem, tm_o = tmem + 256;  // S: 2 x 64 columns a tile, in turn; O: D columns a tile
 
-  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+  if (warp >= kLoadWarp && warp < kSoftmaxWarp) {
     // ---- packed codes and params: one warp for the keys' ring, one for the values' ---------
     const int ring = warp - kLoadWarp;
     const uint32_t base = sm + (ring ? L::values : L::keys), stage_bytes = ring ? L::kValueStage : L::kKeyStage;
     const int P = a.cache.page_size;
-    const int piece = min(kHalf, P & -P), pieces = kHalf / piece;
+    const int piece = min(kKeys, P & -P), pieces = kKeys / piece;
     const int arr = lane / pieces, pc = lane % pieces;  // 0 codes, 1 params, 2 (keys' ring) the values' params
     const int arrays = ring ? 2 : 3;
     const uint32_t bytes = arr == 0 ? piece * (D / 2) : piece * (G * 4);
@@ -413,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    : (ring || arr == 2 ? a.cache.params[1] : a.cache.params[0]);
     int issued = 0;
 #pragma unroll 1
-    for (int i = 0; i < 2 * total; ++i) {
+    for (int i = 0; i < total; ++i) {
       int page = -1, in_page = 0;
-      const int t = first_step * kKeys + i * kHalf + pc * piece;
+      const int t = first_step * kKeys + i * kKeys + pc * piece;
       if (arr < arrays && t < job.len) {
         const int pi = (int)kv4_page(a.cache, (uint32_t)t >> 4);
         in_page = t - pi * P;
@@ -442,41 +436,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     // no copy in flight outlives the CTA
     for (int i = max(0, issued - kRaw); i < issued; ++i)
       mbar_wait(smem_u32(&raw_full[ring][i % kRaw]), i / kRaw & 1, &g_status_prompt, kSiteDrain);
-  } else if (warp == kMmaWarp) {
-    // ---- tensor cores ---------------------------------------------------------
+  } else if (warp < kLoadWarp) {
+    // ---- tensor cores, row tile `warp` ---------------------------------------------------------
     // The whole warp runs this with warp-uniform operands and one elected lane issues: from a branch of one lane the
     // operands go through vector registers and an MMA costs 175 cycles instead of 65.
     constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys), kIdescO = idesc_f16_f32(128, D);
     // descriptors of the operands' first blocks; a step along K or a block further only adds to the address field
     const uint64_t dq = sdesc_sw128(sm + L::q), dk = sdesc_sw128(sm + L::k), dv = sdesc_sw128(sm + L::v);
     const uint32_t um_s = __shfl_sync(0xffffffffu, tm_s, 0), um_o = __shfl_sync(0xffffffffu, tm_o, 0);
-    const auto scores = [&](int t, int buf) {
-      const uint64_t q = dq + (uint32_t)t * (L::kOperand >> 4), k = dk + (uint32_t)buf * (L::kOperand >> 4);
-      const uint32_t d = um_s + t * 128;
+    const int t = __shfl_sync(0xffffffffu, warp, 0), mine = steps[t];
+    const auto scores = [&](int i) {
+      const uint64_t q = dq + (uint32_t)t * (L::kOperand >> 4), k = dk + (uint32_t)(i % kBuf) * (L::kStep >> 4);
+      const uint32_t d = um_s + (i & 1) * 64 + t * 128;
       if (elect_one()) {
         mma_first(d, q, k, kIdescS);
 #pragma unroll
-        for (int i = 1; i < 4 * G; ++i)
-          mma_next(d, q + (uint32_t)((i / 4 * L::kBlock + i % 4 * 32) >> 4), k + (uint32_t)((i / 4 * L::kBlock + i % 4 * 32) >> 4),
-                   kIdescS);
-        mma_commit(smem_u32(&s_full[t]));
+        for (int n = 1; n < 4 * G; ++n)
+          mma_next(d, q + (uint32_t)((n / 4 * L::kBlock + n % 4 * 32) >> 4),
+                   k + (uint32_t)((n / 4 * (kKeys * 128) + n % 4 * 32) >> 4), kIdescS);
+        mma_commit(smem_u32(&s_full[t][i & 1]));
+        mma_commit(smem_u32(&k_empty[i % kBuf]));
       }
       __syncwarp();
     };
-    const auto outputs = [&](int t, int buf, bool more) {
-      const uint64_t v = dv + (uint32_t)buf * (L::kOperand >> 4);
-      const uint32_t d = um_o + t * D, p = um_s + t * 128;
+    const auto outputs = [&](int i) {
+      const uint64_t v = dv + (uint32_t)(i % kBuf) * (L::kStep >> 4);
+      const uint32_t d = um_o + t * D, p = um_s + (i & 1) * 64 + t * 128;
       if (elect_one()) {
-        mma_f16_ts(d, p, v, kIdescO, more);
+        mma_f16_ts(d, p, v, kIdescO, i > 0);
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
-          mma_next_ts(d, p + i * 8, v + (uint32_t)((i / 4 * (D * 128) + i % 4 * 32) >> 4), kIdescO);
-        mma_commit(smem_u32(&o_done[t]));
+        for (int n = 1; n < 4; ++n) mma_next_ts(d, p + n * 8, v + (uint32_t)(n * 32 >> 4), kIdescO);
+        mma_commit(smem_u32(&o_done[t][i & 1]));
+        mma_commit(smem_u32(&v_empty[i % kBuf]));
       }
-      __syncwarp();
-    };
-    const auto commit = [&](uint64_t& bar) {
-      if (elect_one()) mma_commit(smem_u32(&bar));
       __syncwarp();
     };
     const auto wait = [&](uint64_t& bar, int parity, uint32_t site) {
@@ -484,35 +476,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return ok;
     };
-    bool ok = total == 0 || wait(k_full[0], 0, kSiteKFull);
-    if (ok && total > 0) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (steps[t] > 0) scores(t, 0);
-      commit(k_empty[0]);
-    }
+    // Scores run two steps ahead of the outputs, into the columns whose P the product before them has read (the
+    // tensor cores work in order): a tile's next scores are there when its softmax comes to them.
+    bool ok = true;
 #pragma unroll 1
-    for (int j = 0; j < total && ok; ++j) {
-      const int buf = j & 1, par = j >> 1 & 1;
-      ok = wait(v_full[buf], par, kSiteVFull);
-      bool keys = false;  // the next step's have come
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && j < steps[t]) {
-          ok = wait(p_full[t], j & 1, kSiteP);
-          if (!ok) break;
-          outputs(t, buf, j > 0);
-          if (j + 1 < steps[t]) {
-            if (!keys) ok = wait(k_full[buf ^ 1], (j + 1) >> 1 & 1, kSiteKFull);
-            if (!ok) break;
-            keys = true;
-            scores(t, buf ^ 1);  // in order behind the product that reads P from the same columns
-          }
-        }
-      commit(v_empty[buf]);
-      if (j + 1 < total) commit(k_empty[buf ^ 1]);
+    for (int i = -2; i < mine && ok; ++i) {
+      const int next = i + 2;
+      if (i >= 0) {
+        ok = wait(v_full[i % kBuf], i / kBuf & 1, kSiteVFull) && wait(p_full[t][i & 1], i >> 1 & 1, kSiteP);
+        if (ok) outputs(i);
+      }
+      if (ok && next < mine) {
+        ok = wait(k_full[next % kBuf], next / kBuf & 1, kSiteKFull);
+        if (ok) scores(next);
+      }
     }
-    commit(drained);
+    // the other tile's further steps want this one's part of their barriers (once the step's own phase has begun)
+#pragma unroll 1
+    for (int i = mine; i < total && ok; ++i) {
+      ok = wait(k_full[i % kBuf], i / kBuf & 1, kSiteKFull) && wait(v_full[i % kBuf], i / kBuf & 1, kSiteVFull);
+      if (ok && lane == 0) {
+        mbar_arrive(smem_u32(&k_empty[i % kBuf]));
+        mbar_arrive(smem_u32(&v_empty[i % kBuf]));
+      }
+    }
+    if (elect_one()) mma_commit(smem_u32(&drained));
+    __syncwarp();
     mbar_wait(smem_u32(&drained), 0, &g_status_prompt, kSiteDrain);
     __syncwarp();
   } else if (warp >= kValueWarp) {
@@ -522,16 +511,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int swap = tg & 1;  // odd groups read their pairs the other way round: no bank twice
     const uint32_t sel_lo = swap ? 0x1054u : 0x5410u, sel_hi = swap ? 0x3276u : 0x7632u;
 #pragma unroll 1
-    for (int i = 0; i < 2 * total; ++i) {
-      const int j = i >> 1, half = i & 1, buf = j & 1, st = i % kRaw;
-      bool ok = true;
-      if (half == 0) ok = mbar_wait(smem_u32(&v_empty[buf]), (j >> 1 & 1) ^ 1, &g_status_prompt, kSiteVEmpty);
+    for (int i = 0; i < total; ++i) {
+      const int buf = i % kBuf, st = i % kRaw;
+      bool ok = mbar_wait(smem_u32(&v_empty[buf]), (i / kBuf & 1) ^ 1, &g_status_prompt, kSiteVEmpty);
       if (ok) ok = mbar_wait(smem_u32(&raw_full[1][st]), i / kRaw & 1, &g_status_prompt, kSiteRawFull);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* vc = smp + L::values + st * L::kValueStage;
       const uint8_t* vp = vc + L::kCodes;
-      const int t0 = (first_step + j) * kKeys + half * kHalf;
-      const bool odd = any_odd<kHalf * G>(vp, lane) || t0 < lo || t0 + kHalf > job.len;
+      const int t0 = (first_step + i) * kKeys;
+      const bool odd = any_odd<kKeys * G>(vp, lane) || t0 < lo || t0 + kKeys > job.len;
       if (G == 2 || dt < 64) {
         uint32_t pw[8];
 #pragma unroll
@@ -565,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < 4; ++p) out[c][p] = h2_finite(out[c][p]);
         }
-        // row 64 g + 8 i + jw, keys half * 64 + tg * 8 ..: block `half`, chunk tg
-        const uint32_t vrow = sm + L::v + buf * L::kOperand + half * (D * 128) + (64 * g + jw) * 128 + ((tg ^ jw) << 4);
+        // row 64 g + 8 i + jw, keys 8 tg ..: chunk tg
+        const uint32_t vrow = sm + L::v + buf * L::kStep + (64 * g + jw) * 128 + ((tg ^ jw) << 4);
 #pragma unroll
         for (int i2 = 0; i2 < 8; ++i2) sts128(vrow + i2 * 8 * 128, out[i2][0], out[i2][1], out[i2][2], out[i2][3]);
       }
@@ -574,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(smem_u32(&raw_empty[1][st]));
-        if (half == 1) mbar_arrive(smem_u32(&v_full[buf]));
+        mbar_arrive(smem_u32(&v_full[buf]));
       }
     }
   } else if (warp >= kKeyWarp) {
@@ -582,15 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int dt = tid - 32 * kKeyWarp;
     constexpr int kParts = D / 32;  // lanes per token
 #pragma unroll 1
-    for (int i = 0; i < 2 * total; ++i) {
-      const int j = i >> 1, half = i & 1, buf = j & 1, st = i % kRaw;
-      bool ok = true;
-      if (half == 0) ok = mbar_wait(smem_u32(&k_empty[buf]), (j >> 1 & 1) ^ 1, &g_status_prompt, kSiteKEmpty);
+    for (int i = 0; i < total; ++i) {
+      const int buf = i % kBuf, st = i % kRaw;
+      bool ok = mbar_wait(smem_u32(&k_empty[buf]), (i / kBuf & 1) ^ 1, &g_status_prompt, kSiteKEmpty);
       if (ok) ok = mbar_wait(smem_u32(&raw_full[0][st]), i / kRaw & 1, &g_status_prompt, kSiteRawFull);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* kc = smp + L::keys + st * L::kKeyStage;
       const uint8_t *kp = kc + L::kCodes, *vp = kp + L::kParams;
-      const bool odd = any_odd<2 * kHalf * G>(kp, lane);  // the values' params lie behind the keys'
+      const bool odd = any_odd<2 * kKeys * G>(kp, lane);  // the values' params lie behind the keys'
 #pragma unroll
       for (int it = 0; it < kParts / 2; ++it) {
         const int item = dt + 128 * it, part = item % kParts, tok = item / kParts;
@@ -625,25 +612,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int m = 0; m < 4; ++m) out[k][m] = bad ? 0x7FFF7FFFu : h2_finite(out[k][m]);
         }
         // word k of the lane is word [j, g] of the token: index part * 4 + k = j G + g
-        const uint32_t krow = sm + L::k + buf * L::kOperand + (half * kHalf + tok) * 128;
+        const uint32_t krow = sm + L::k + buf * L::kStep + tok * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int jw = (part * 4 + k) / G;
-          sts128(krow + (k % G) * L::kBlock + ((jw ^ (tok & 7)) << 4), out[k][0], out[k][1], out[k][2], out[k][3]);
+          sts128(krow + (k % G) * (kKeys * 128) + ((jw ^ (tok & 7)) << 4), out[k][0], out[k][1], out[k][2], out[k][3]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(smem_u32(&raw_empty[0][st]));
-        if (half == 1) mbar_arrive(smem_u32(&k_full[buf]));
+        mbar_arrive(smem_u32(&k_full[buf]));
       }
     }
   } else if (warp >= kSoftmaxWarp) {
     // ---- softmax, one thread per row ------------------------------------------
     const int mine = steps[tile];
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor-memory lane 32 (warp % 4)
-    const uint32_t ts = tm_s + tile * 128 + lanes, to = tm_o + tile * D + lanes;
+    const uint32_t to = tm_o + tile * D + lanes;
     const int last_row = min(row0 + 128 * tile + 127, job.rows - 1);
     const int r = min(row, last_row);  // rows behind the last: zero queries with its mask
     const int end = end_of(r), beg = beg_of(r);
@@ -652,13 +639,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < mine; ++j) {
-      ok = mbar_wait(smem_u32(&s_full[tile]), j & 1, &g_status_prompt, kSiteS);
+      const uint32_t ts = tm_s + tile * 128 + (j & 1) * 64 + lanes;
+      ok = mbar_wait(smem_u32(&s_full[tile][j & 1]), j >> 1 & 1, &g_status_prompt, kSiteS);
+      // the product of step j - 2 came before these scores; its barrier is taken phase by phase
+      if (ok && j >= 2) ok = mbar_wait(smem_u32(&o_done[tile][j & 1]), (j - 2) >> 1 & 1, &g_status_prompt, kSiteO);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const int t0 = (first_step + j) * kKeys;
       const bool full = t0 >= max_beg && t0 + kKeys <= min_end;
       const int cb = beg - t0, ce = end - t0;  // the visible columns [cb, ce)
-      const float top = full ? row_max<true>(ts, cb, ce) : row_max<false>(ts, cb, ce);
+      uint32_t v[2][32];
+      tmem_ld32(ts, v[0]);
+      tmem_ld32(ts + 32, v[1]);
+      tmem_ld_wait();
+      const float top = full ? row_max<true>(v, cb, ce) : row_max<false>(v, cb, ce);
       const bool far = top > -INFINITY && (m == -INFINITY || (top - m) * sigma > kAhead);
       if (__any_sync(0xffffffffu, far)) {
         const float mn = fmaxf(m, top);
@@ -667,27 +661,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         mneg = m == -INFINITY ? 0.0f : fmaf(-m, sigma, kLift);
         l *= corr;
         if (j > 0) {
-          ok = mbar_wait(smem_u32(&o_done[tile]), (j - 1) & 1, &g_status_prompt, kSiteO);
+          ok = mbar_wait(smem_u32(&o_done[tile][(j - 1) & 1]), (j - 1) >> 1 & 1, &g_status_prompt, kSiteO);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
-            uint32_t v[16];
-            tmem_ld16(to + 16 * c, v);
+            uint32_t u[16];
+            tmem_ld16(to + 16 * c, u);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
-            tmem_st16(to + 16 * c, v);
+            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * corr);
+            tmem_st16(to + 16 * c, u);
           }
         }
       }
-      l += full ? row_exp<true>(ts, sigma, mneg, cb, ce) : row_exp<false>(ts, sigma, mneg, cb, ce);
+      l += full ? row_exp<true>(v, ts, sigma, mneg, cb, ce) : row_exp<false>(v, ts, sigma, mneg, cb, ce);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(smem_u32(&p_full[tile]));
+      mbar_arrive(smem_u32(&p_full[tile][j & 1]));
     }
     // the output row
-    if (mine > 0 && ok) ok = mbar_wait(smem_u32(&o_done[tile]), (mine - 1) & 1, &g_status_prompt, kSiteO);
+    for (int j = max(0, mine - 2); j < mine && ok; ++j)
+      ok = mbar_wait(smem_u32(&o_done[tile][j & 1]), j >> 1 & 1, &g_status_prompt, kSiteO);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     const bool valid = row < job.rows;

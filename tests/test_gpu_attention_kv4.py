@@ -383,3 +383,21 @@ def test_merging_by_the_log_sum_exp():
     ref, _, bound, _ = attention_ref(qs, cache, table, [L], [1], 0.125)
     tol = torch.from_numpy(3 * bound).cuda() + 3 * 2.0 ** -11 * (wa * a.abs() + wb * b.abs() + w.abs())
     assert ((wa * a + wb * b - w).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n,L", [(300, 300), (513, 700), (1024, 1024), (256, 3000), (130, 6000)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_prompts(n, L, D):
+    """Many steps over the keys by both row tiles, one share of the keys a block (many heads) and several (one)."""
+    _run([L], [n], 2, 1, D, 64, F16, seed=n)
+    q = qg()
+    table, pages = paged([L], 64, 1)
+    one = random_cache(q, pages, 1, D, 64, 1)
+    many = q.KV4Cache(*(t.expand(-1, 160, *t.shape[2:]).contiguous() for t in one))
+    qs = torch.randn(n, 1, D, device="cuda").to(F16)
+    args = torch.from_numpy(table).cuda(), torch.tensor([L], dtype=torch.int32, device="cuda")
+    x = q.attention_kv4(qs.expand(-1, 160, -1).contiguous(), many, *args)
+    q.check_device_errors()
+    ref, _, bound, _ = attention_ref(qs, one, table, [L], [n], D ** -0.5)
+    assert_attention(x[:, :1], ref, bound)
+    assert torch.equal(x, x[:, :1].expand(-1, 160, -1))
