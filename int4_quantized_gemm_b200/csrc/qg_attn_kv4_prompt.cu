@@ -56,6 +56,10 @@ constexpr int kKeys = 64;       // keys per step
 constexpr int kBuf = 4;         // buffers of dequantized keys and values
 constexpr int kRaw = 3;         // raw stages
 constexpr int kThreads = 640;
+// Registers a thread: 96 at launch (65536 / 640); then 128 for the softmax warps, 80 for the warps that dequantize and
+// 64 for the others: 256 * 128 + 256 * 80 + 128 * 64 = 640 * 96.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kDequantRegs = 80, kOtherRegs = 64;
+static_assert(256 * kSoftmaxRegs + 256 * kDequantRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "");
 // Warps 0 and 1 issue the products of a row tile each, 2 and 3 load keys and values.  (One warp for both tiles spent
 // half of its time between the products, in waits whose barriers had long completed.)
 constexpr int kMmaWarp = 0, kLoadWarp = 2, kSoftmaxWarp = 4, kKeyWarp = 12, kValueWarp = 16;
@@ -63,7 +67,7 @@ constexpr float kLift = 7.0f, kAhead = 8.0f;
 
 enum : uint32_t {
   kSiteSequence = 1, kSitePage, kSiteRawFull, kSiteRawEmpty, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty,
-  kSiteS, kSiteP, kSiteO, kSiteDrain
+  kSiteS, kSiteP, kSiteO, kSiteQ, kSiteDrain
 };
 
 __device__ __forceinline__ void report(uint32_t code, uint32_t site) {
@@ -229,6 +233,15 @@ struct Layout {
   static constexpr uint32_t bytes = values + kRaw * kValueStage;
 };
 
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // The largest of a row's 64 scores (kAll: all of them, else columns [cb, ce)).
 template <bool kAll>
 __device__ __forceinline__ float row_max(const uint32_t (&v)[2][32], int cb, int ce) {
@@ -289,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int D = L::D;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t raw_full[2][kRaw], raw_empty[2][kRaw], k_full[kBuf], k_empty[kBuf],
-      v_full[kBuf], v_empty[kBuf], s_full[2][2], p_full[2][2], o_done[2][2], drained;
+      v_full[kBuf], v_empty[kBuf], s_full[2][2], p_full[2][2], o_done[2][2], q_full[2], drained;
   __shared__ uint32_t tmem_slot;
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smp = smem_raw + (sm - smem_u32(smem_raw));
@@ -309,6 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&p_full[0][i]), 128);
       mbar_init(smem_u32(&o_done[0][i]), 1);
     }
+    mbar_init(smem_u32(&q_full[0]), 4);
+    mbar_init(smem_u32(&q_full[1]), 4);
     mbar_init(smem_u32(&drained), 2);
     fence_mbar_init();
   }
@@ -346,53 +361,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_step = step0 + j0;
   const int lo = min(beg_of(row0), job.len);  // the oldest key that any row sees
 
-  // --- queries: a thread per row, scaled by a power of two to fp16 -------------
-  float sigma = 0.0f;
-  const int tile = (warp - kSoftmaxWarp) / 4 & 1, st_row = tid - 32 * kSoftmaxWarp, row = row0 + st_row;  // softmax warps
-  if (warp >= kSoftmaxWarp && warp < kKeyWarp) {
-    uint4 v[D / 8];
-    float amax = 0.0f;
-    if (row < job.rows) {
-      const int t = job.first + row / a.group, hq = job.h * a.group + row % a.group;
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + 2 * (t * a.q_st + hq * a.q_sh));
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = p[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    const auto values = [&](uint32_t b) {
-      return a.dtype == QG_F16 ? half2_f32(b) : make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
-    };
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      const uint32_t* pv = &v[i].x;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = values(pv[k]);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-    }
-    int e = 8 - ((int)(__float_as_uint(amax) >> 23) - 127);
-    e = max(-100, min(100, e));
-    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-    sigma = a.scale * 1.44269504088896f * __uint_as_float((uint32_t)(127 - e) << 23);
-    const uint32_t qrow = sm + L::q + tile * L::kOperand + (st_row & 127) * 128;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      const float2 f0 = values(v[i].x), f1 = values(v[i].y), f2 = values(v[i].z), f3 = values(v[i].w);
-      sts128(qrow + (i / 8) * L::kBlock + (((i & 7) ^ (st_row & 7)) << 4), half2_bits(f0.x * up, f2.x * up),
-             half2_bits(f0.y * up, f2.y * up), half2_bits(f1.x * up, f3.x * up), half2_bits(f1.y * up, f3.y * up));
-    }
-    fence_proxy_async_smem();
-  }
   tc_fence_before();
   cta_barrier_all();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint32_t tm_s = tmem, tm_o = tmem + 256;  // S: 2 x 64 columns a tile, in turn; O: D columns a tile
 
-  if (warp >= kLoadWarp && warp < kSoftmaxWarp) {
+  // each group of four warps changes its registers at the head of its own branch
+  if (warp < kSoftmaxWarp) {
+   regs_down<kOtherRegs>();
+   if (warp >= kLoadWarp) {
     // ---- packed codes and params: one warp for the keys' ring, one for the values' ---------
     const int ring = warp - kLoadWarp;
     const uint32_t base = sm + (ring ? L::values : L::keys), stage_bytes = ring ? L::kValueStage : L::kKeyStage;
@@ -436,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // no copy in flight outlives the CTA
     for (int i = max(0, issued - kRaw); i < issued; ++i)
       mbar_wait(smem_u32(&raw_full[ring][i % kRaw]), i / kRaw & 1, &g_status_prompt, kSiteDrain);
-  } else if (warp < kLoadWarp) {
+   } else {
     // ---- tensor cores, row tile `warp` ---------------------------------------------------------
     // The whole warp runs this with warp-uniform operands and one elected lane issues: from a branch of one lane the
     // operands go through vector registers and an MMA costs 175 cycles instead of 65.
@@ -478,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Scores run two steps ahead of the outputs, into the columns whose P the product before them has read (the
     // tensor cores work in order): a tile's next scores are there when its softmax comes to them.
-    bool ok = true;
+    bool ok = mine == 0 || wait(q_full[t], 0, kSiteQ);
 #pragma unroll 1
     for (int i = -2; i < mine && ok; ++i) {
       const int next = i + 2;
@@ -504,7 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mbar_wait(smem_u32(&drained), 0, &g_status_prompt, kSiteDrain);
     __syncwarp();
+   }
   } else if (warp >= kValueWarp) {
+    regs_down<kDequantRegs>();
     // ---- values to fp16: a lane takes one word (8 channels) of 8 tokens and writes 8 tokens of 8 channels ----
     const int dt = tid - 32 * kValueWarp;
     const int jw = dt & 7, g = G == 2 ? dt >> 3 & 1 : 0, tg = dt >> (G == 2 ? 4 : 3);
@@ -566,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= kKeyWarp) {
+    regs_down<kDequantRegs>();
     // ---- keys to fp16: a lane takes 4 words (32 channels) of a token ----------------------------
     const int dt = tid - 32 * kKeyWarp;
     constexpr int kParts = D / 32;  // lanes per token
@@ -626,8 +607,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(smem_u32(&k_full[buf]));
       }
     }
-  } else if (warp >= kSoftmaxWarp) {
+  } else {
+    regs_up<kSoftmaxRegs>();
     // ---- softmax, one thread per row ------------------------------------------
+    const int tile = (warp - kSoftmaxWarp) / 4, wrow = (warp & 3) * 32;  // the warp's rows in its tile
+    const int row = row0 + tile * 128 + wrow + lane;
+    const bool valid = row < job.rows;
+    const int t_row = job.first + row / a.group, hq = job.h * a.group + row % a.group;
+    // Rows move 16 bytes a lane, kLpr lanes a row; a lane knows its own row's place.
+    constexpr int kLpr = D / 8, kRpi = 32 / kLpr;
+    const int piece = lane % kLpr, sub = lane / kLpr;
+    const uint32_t place = sm + L::q + tile * L::kOperand + (piece / 8) * L::kBlock;  // of the lane's 16 bytes in row 0
+    const auto in_row = [&](int r) { return place + (wrow + r) * 128 + (((piece & 7) ^ (r & 7)) << 4); };
+    // queries: scaled by a power of two to fp16, a row's largest near 2^8
+    float sigma = 0.0f;
+    {
+      const int64_t mine_at = valid ? 2 * (t_row * a.q_st + hq * a.q_sh) : -1;
+      uint4 v[kLpr];
+#pragma unroll
+      for (int it = 0; it < kLpr; ++it) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine_at, it * kRpi + sub);
+        v[it] = at < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                       : __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + at + 16 * piece));
+      }
+#pragma unroll
+      for (int it = 0; it < kLpr; ++it) {
+        const uint32_t* pv = &v[it].x;
+        float2 f[4];
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[k] = a.dtype == QG_F16 ? half2_f32(pv[k])
+                                   : make_float2(__uint_as_float(pv[k] << 16), __uint_as_float(pv[k] & 0xffff0000u));
+          amax = fmaxf(amax, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+        }
+#pragma unroll
+        for (int d = 1; d < kLpr; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        int e = 8 - ((int)(__float_as_uint(amax) >> 23) - 127);
+        e = max(-100, min(100, e));
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        const float down = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(127 - e) << 23), lane % kRpi * kLpr);
+        if (lane / kRpi == it) sigma = a.scale * 1.44269504088896f * down;  // the lane's own row
+        sts128(in_row(it * kRpi + sub), half2_bits(f[0].x * up, f[2].x * up), half2_bits(f[0].y * up, f[2].y * up),
+               half2_bits(f[1].x * up, f[3].x * up), half2_bits(f[1].y * up, f[3].y * up));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&q_full[tile]));
+    }
     const int mine = steps[tile];
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor-memory lane 32 (warp % 4)
     const uint32_t to = tm_o + tile * D + lanes;
@@ -685,10 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait(smem_u32(&o_done[tile][j & 1]), j >> 1 & 1, &g_status_prompt, kSiteO);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    const bool valid = row < job.rows;
-    const int t = job.first + row / a.group, hq = job.h * a.group + row % a.group;
-    const int64_t flat = (int64_t)job.split * a.T * a.heads_q + (int64_t)t * a.heads_q + hq;
+    const int64_t flat = (int64_t)job.split * a.T * a.heads_q + (int64_t)t_row * a.heads_q + hq;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const uint32_t my_row = sm + L::q + tile * L::kOperand + (wrow + lane) * 128;  // the queries have been read
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float v[64];
@@ -706,39 +732,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i) v[i] = 0.0f;
       }
-      if (valid && ok) {
-        // column 8 i + jw is channel 8 jw + i
-        if (splits == 1) {
-          char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + 64 * g);
+      // column 8 i + jw is channel 8 jw + i
+      if (splits == 1) {
 #pragma unroll
-          for (int jw = 0; jw < 8; ++jw) {
-            uint32_t b[4];
+        for (int jw = 0; jw < 8; ++jw) {
+          uint32_t b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x = v[16 * i + jw] * inv, y = v[16 * i + 8 + jw] * inv;
-              if (a.dtype == QG_F16) {
-                b[i] = half2_bits(x, y);
-              } else {
-                __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-                b[i] = *reinterpret_cast<uint32_t*>(&h);
-              }
+          for (int i = 0; i < 4; ++i) {
+            const float x = v[16 * i + jw] * inv, y = v[16 * i + 8 + jw] * inv;
+            if (a.dtype == QG_F16) {
+              b[i] = half2_bits(x, y);
+            } else {
+              __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+              b[i] = *reinterpret_cast<uint32_t*>(&h);
             }
-            *reinterpret_cast<uint4*>(p + 16 * jw) = make_uint4(b[0], b[1], b[2], b[3]);
           }
-        } else {
-          float* p = parts.sums + flat * D + 64 * g;
-#pragma unroll
-          for (int jw = 0; jw < 8; ++jw) {
-            *reinterpret_cast<float4*>(p + 8 * jw) = make_float4(v[jw], v[8 + jw], v[16 + jw], v[24 + jw]);
-            *reinterpret_cast<float4*>(p + 8 * jw + 4) = make_float4(v[32 + jw], v[40 + jw], v[48 + jw], v[56 + jw]);
-          }
+          sts128(my_row + g * L::kBlock + ((jw ^ (lane & 7)) << 4), b[0], b[1], b[2], b[3]);
         }
+      } else if (valid && ok) {
+        float* p = parts.sums + flat * D + 64 * g;
+#pragma unroll
+        for (int jw = 0; jw < 8; ++jw) {
+          *reinterpret_cast<float4*>(p + 8 * jw) = make_float4(v[jw], v[8 + jw], v[16 + jw], v[24 + jw]);
+          *reinterpret_cast<float4*>(p + 8 * jw + 4) = make_float4(v[32 + jw], v[40 + jw], v[48 + jw], v[56 + jw]);
+        }
+      }
+    }
+    if (splits == 1) {
+      __syncwarp();
+      const int64_t mine_at = valid && ok ? 2 * (t_row * a.o_st + hq * a.o_sh) : -1;
+#pragma unroll
+      for (int it = 0; it < kLpr; ++it) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine_at, it * kRpi + sub);
+        uint4 o;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "r"(in_row(it * kRpi + sub)));
+        if (at >= 0) *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + at + 16 * piece) = o;
       }
     }
     if (valid && ok) {
       const float lg = l == 0.0f ? -INFINITY : m * sigma - kLift;  // log2 of what p was taken against
       if (splits > 1) parts.ml[flat] = make_float2(lg, l);
-      else if (a.lse) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (lg + log2f(l)) * 0.69314718056f;
+      else if (a.lse) a.lse[(int64_t)t_row * a.heads_q + hq] = l == 0.0f ? -INFINITY : (lg + log2f(l)) * 0.69314718056f;
     }
     tc_fence_before();
   }
@@ -816,6 +850,11 @@ qg_status launch(const Attn4& a, int min_rows, void* workspace, cudaStream_t s) 
   constexpr int kSmem = Layout<G>::bytes + 1024;
   static PerDeviceOnce once;
   const qg_status st = once.run([](int) {
+    // the warps' register shares are drawn on the block's own: fewer at launch would wait for ever
+    cudaFuncAttributes f;
+    const qg_status q = check_cuda(cudaFuncGetAttributes(&f, attention_kv4_prompt<G>), "attention_kv4 attributes");
+    if (q != QG_OK) return q;
+    if (f.numRegs < kLaunchRegs) return fail(QG_ERR_UNSUPPORTED, "attention_kv4: built with %d registers a thread, %d needed", f.numRegs, kLaunchRegs);
     return check_cuda(cudaFuncSetAttribute(attention_kv4_prompt<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
                       "attention_kv4 shared memory");
   });
