@@ -56,9 +56,9 @@ constexpr int kKeys = 64;       // keys per step
 constexpr int kBuf = 4;         // buffers of dequantized keys and values
 constexpr int kRaw = 3;         // raw stages
 constexpr int kThreads = 640;
-// Registers a thread: 96 at launch (65536 / 640); then 128 for the softmax warps, 80 for the warps that dequantize and
-// 64 for the others: 256 * 128 + 256 * 80 + 128 * 64 = 640 * 96.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kDequantRegs = 80, kOtherRegs = 64;
+// Registers a thread: 96 at launch (65536 / 640); then 144 for the softmax warps, 72 for the warps that dequantize and
+// 48 for the others: 256 * 144 + 256 * 72 + 128 * 48 = 640 * 96.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 144, kDequantRegs = 72, kOtherRegs = 48;
 static_assert(256 * kSoftmaxRegs + 256 * kDequantRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "");
 // Warps 0 and 1 issue the products of a row tile each, 2 and 3 load keys and values.  (One warp for both tiles spent
 // half of its time between the products, in waits whose barriers had long completed.)
@@ -85,7 +85,6 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-__device__ __forceinline__ float2 half2_f32(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
 __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -610,51 +609,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     regs_up<kSoftmaxRegs>();
     // ---- softmax, one thread per row ------------------------------------------
-    const int tile = (warp - kSoftmaxWarp) / 4, wrow = (warp & 3) * 32;  // the warp's rows in its tile
+    // Rows move 16 bytes a lane, kLpr lanes a row; a lane knows the place of its own row, whose softmax it takes.
+    constexpr int kLpr = D / 8, kRpi = 32 / kLpr;
+    const int tile = (warp - kSoftmaxWarp) / 4 & 1, wrow = (warp & 3) * 32;  // the warp's rows in its tile
     const int row = row0 + tile * 128 + wrow + lane;
     const bool valid = row < job.rows;
     const int t_row = job.first + row / a.group, hq = job.h * a.group + row % a.group;
-    // Rows move 16 bytes a lane, kLpr lanes a row; a lane knows its own row's place.
-    constexpr int kLpr = D / 8, kRpi = 32 / kLpr;
     const int piece = lane % kLpr, sub = lane / kLpr;
-    const uint32_t place = sm + L::q + tile * L::kOperand + (piece / 8) * L::kBlock;  // of the lane's 16 bytes in row 0
-    const auto in_row = [&](int r) { return place + (wrow + r) * 128 + (((piece & 7) ^ (r & 7)) << 4); };
-    // queries: scaled by a power of two to fp16, a row's largest near 2^8
-    float sigma = 0.0f;
+    uint4 qv[kLpr];
     {
       const int64_t mine_at = valid ? 2 * (t_row * a.q_st + hq * a.q_sh) : -1;
-      uint4 v[kLpr];
 #pragma unroll
       for (int it = 0; it < kLpr; ++it) {
         const int64_t at = __shfl_sync(0xffffffffu, mine_at, it * kRpi + sub);
-        v[it] = at < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                       : __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + at + 16 * piece));
+        qv[it] = at < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                        : __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + at + 16 * piece));
       }
+    }
+    const uint32_t place = sm + L::q + tile * L::kOperand + (piece / 8) * L::kBlock;  // of the lane's 16 bytes in row 0
+    const auto in_row = [&](int r) { return place + (wrow + r) * 128 + (((piece & 7) ^ (r & 7)) << 4); };
+    // queries to fp16: as they are, or (bf16) scaled by a power of two that brings the warp's largest near 2^8
+    float sigma = a.scale * 1.44269504088896f;
+    if (a.dtype == QG_F16) {
+#pragma unroll
+      for (int it = 0; it < kLpr; ++it)
+        sts128(in_row(it * kRpi + sub), __byte_perm(qv[it].x, qv[it].z, 0x5410), __byte_perm(qv[it].x, qv[it].z, 0x7632),
+               __byte_perm(qv[it].y, qv[it].w, 0x5410), __byte_perm(qv[it].y, qv[it].w, 0x7632));
+    } else {
+      uint32_t most = 0;  // of the magnitudes' bits
 #pragma unroll
       for (int it = 0; it < kLpr; ++it) {
-        const uint32_t* pv = &v[it].x;
-        float2 f[4];
-        float amax = 0.0f;
+        const uint32_t* w = &qv[it].x;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[k] = a.dtype == QG_F16 ? half2_f32(pv[k])
-                                   : make_float2(__uint_as_float(pv[k] << 16), __uint_as_float(pv[k] & 0xffff0000u));
-          amax = fmaxf(amax, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-        }
-#pragma unroll
-        for (int d = 1; d < kLpr; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        int e = 8 - ((int)(__float_as_uint(amax) >> 23) - 127);
-        e = max(-100, min(100, e));
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        const float down = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(127 - e) << 23), lane % kRpi * kLpr);
-        if (lane / kRpi == it) sigma = a.scale * 1.44269504088896f * down;  // the lane's own row
-        sts128(in_row(it * kRpi + sub), half2_bits(f[0].x * up, f[2].x * up), half2_bits(f[0].y * up, f[2].y * up),
-               half2_bits(f[1].x * up, f[3].x * up), half2_bits(f[1].y * up, f[3].y * up));
+        for (int k = 0; k < 4; ++k) most = max(most, max(w[k] << 16 & 0x7FFF0000u, w[k] & 0x7FFF0000u));
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&q_full[tile]));
+      most = __reduce_max_sync(0xffffffffu, most);
+      const int e = max(-100, min(100, 8 - ((int)(most >> 23) - 127)));
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      sigma *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int it = 0; it < kLpr; ++it) {
+        const uint32_t* w = &qv[it].x;
+        const auto pair = [&](int i, int k) {  // values i and k
+          const float x = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+          const float y = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+          return half2_bits(x * up, y * up);
+        };
+        sts128(in_row(it * kRpi + sub), pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7));
+      }
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&q_full[tile]));
     const int mine = steps[tile];
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor-memory lane 32 (warp % 4)
     const uint32_t to = tm_o + tile * D + lanes;
