@@ -674,8 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < mine; ++j) {
       const uint32_t ts = tm_s + tile * 128 + (j & 1) * 64 + lanes;
       ok = mbar_wait(smem_u32(&s_full[tile][j & 1]), j >> 1 & 1, &g_status_prompt, kSiteS);
-      // the product of step j - 2 came before these scores; its barrier is taken phase by phase
-      if (ok && j >= 2) ok = mbar_wait(smem_u32(&o_done[tile][j & 1]), (j - 2) >> 1 & 1, &g_status_prompt, kSiteO);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const int t0 = (first_step + j) * kKeys;
@@ -694,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mneg = m == -INFINITY ? 0.0f : fmaf(-m, sigma, kLift);
         l *= corr;
         if (j > 0) {
+          // (of that barrier's phases all but this one are done: step j - 3's product came before step j - 1's scores)
           ok = mbar_wait(smem_u32(&o_done[tile][(j - 1) & 1]), (j - 1) >> 1 & 1, &g_status_prompt, kSiteO);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
