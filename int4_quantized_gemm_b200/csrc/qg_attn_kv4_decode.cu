@@ -64,8 +64,8 @@ namespace {
 // The ring: 64 tokens a stage and 2 stages for each of 12 warps (221 KB at 128 channels, the registers' 168 a thread).
 // 64 sequences of 4096..8192 tokens, 64/8 heads: 125 us; 8 or 10 warps 138, 147; stages of 32 tokens 141.
 constexpr int kChunk = 64;   // tokens per ring stage
-template <int NT>
-constexpr int kWarpsOf = NT == 1 ? 12 : 8;  // workers per CTA (registers: 65536 / (32 workers))
+template <int G, int NT>
+constexpr int kWarpsOf = NT == 2 ? 8 : G == 1 ? 16 : 12;  // workers per CTA (registers: 65536 / (32 workers))
 constexpr int kStages = 2;
 constexpr float kAhead = 8.0f;  // log2 of how far a score may pass the maximum it is taken against
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // fp16x2: -8 2^-24, -128 2^-24
@@ -193,8 +193,7 @@ __host__ __device__ constexpr int part_floats(int nt, int dim) { return 8 * nt *
 
 // What crosses from a CTA into the next ones: the join kernel's work.
 struct Crossing {
-  int b, h, ctas;  // ctas: how many the (sequence, head) spans from this one; 0: none
-  int pad;
+  int first, n, h, ctas;  // the sequence's first query and their number; ctas: how many the item spans from this one, 0: none
 };
 
 // Parts of the two levels and the crossings, in the workspace.
@@ -204,90 +203,98 @@ struct Scratch {
   float* cta_parts;    // [grid][2]
 };
 
-// Adds `count` parts (part(i), called for i = 0, 1, ...) of the 8 rows from `row0` on.  Lane r < 8 holds the log2
-// maximum and the sum of row row0 + r; every lane V values of each row.
+// Adds `count` parts (part(i), i = 0, 1, ...) of a row, a warp: its log2 maximum and sum, and V values in each lane.
+// The parts' weights first, a lane each; no load waits for another part's.
 template <int D, int NT, class F>
-__device__ __forceinline__ void add_parts(F part, int count, int row0, int lane, float& top, float& l,
-                                          float (&v)[8][D / 32]) {
-  constexpr int V = D / 32;
+__device__ __forceinline__ void add_parts(F part, int count, int row, int lane, float& top, float& l,
+                                          float (&v)[D / 32]) {
+  constexpr int V = D / 32, kBatch = 8;
   top = -INFINITY;
   l = 0.0f;
 #pragma unroll
-  for (int r = 0; r < 8; ++r)
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[r][k] = 0.0f;
+  for (int k = 0; k < V; ++k) v[k] = 0.0f;
 #pragma unroll 1
-  for (int i = 0; i < count; ++i) {
-    const float* p = part(i);
-    const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * D + 2 * (row0 + (lane & 7)));
-    float x[8][V];
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const int n = min(32, count - i0);
+    float x[kBatch][V];
+    const auto load = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      if constexpr (V == 4)
-        *reinterpret_cast<float4*>(x[r]) = *reinterpret_cast<const float4*>(p + (row0 + r) * D + V * lane);
-      else
-        *reinterpret_cast<float2*>(x[r]) = *reinterpret_cast<const float2*>(p + (row0 + r) * D + V * lane);
-    }
-    const float t = fmaxf(top, ml.x), safe = t == -INFINITY ? 0.0f : t;
+      for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[b][k] = 0.0f;
+        if (i + b < n) {
+          const float* p = part(i0 + i + b) + row * D + V * lane;
+          if constexpr (V == 4) *reinterpret_cast<float4*>(x[b]) = *reinterpret_cast<const float4*>(p);
+          else *reinterpret_cast<float2*>(x[b]) = *reinterpret_cast<const float2*>(p);
+        }
+      }
+    };
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < n) ml = *reinterpret_cast<const float2*>(part(i0 + lane) + 8 * NT * D + 2 * row);
+    load(0);
+    float t = ml.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+    t = fmaxf(t, top);
+    const float safe = t == -INFINITY ? 0.0f : t;
     const float f = ex2(top - safe), g = ex2(ml.x - safe);
-    l = l * f + ml.y * g;
+    float sum = ml.y * g;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = fmaf(l, f, sum);
     top = t;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float fr = __shfl_sync(0xffffffffu, f, r), gr = __shfl_sync(0xffffffffu, g, r);
+    for (int k = 0; k < V; ++k) v[k] *= f;
+#pragma unroll 1
+    for (int i = 0;;) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[r][k] = fmaf(x[r][k], gr, v[r][k] * fr);
+      for (int b = 0; b < kBatch; ++b) {
+        const float gb = __shfl_sync(0xffffffffu, g, (i + b) & 31);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = fmaf(x[b][k], i + b < n ? gb : 0.0f, v[k]);
+      }
+      i += kBatch;
+      if (i >= n) break;
+      load(i);
     }
   }
 }
 
-// out (and lse) of the rows [row0, rows) of an item from their sums
+// out (and lse) of a row of an item from its sums, a warp
 template <int D>
-__device__ __forceinline__ void write_rows(const Attn4& a, int first, int h, int row0, int rows, int lane, float top,
-                                           float l, const float (&v)[8][D / 32]) {
+__device__ __forceinline__ void write_row(const Attn4& a, int first, int h, int row, int lane, float top, float l,
+                                          const float (&v)[D / 32]) {
   constexpr int V = D / 32;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int t = first + row / a.group, hq = h * a.group + row % a.group;
+  uint32_t b[V / 2];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const float lr = __shfl_sync(0xffffffffu, l, r), ir = __shfl_sync(0xffffffffu, inv, r);
-    const int row = row0 + r;
-    if (row < rows) {
-      const int t = first + row / a.group, hq = h * a.group + row % a.group;
-      uint32_t b[V / 2];
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        const float x = lr == 0.0f ? 0.0f : v[r][2 * i] * ir, y = lr == 0.0f ? 0.0f : v[r][2 * i + 1] * ir;
-        if (a.dtype == QG_F16) {
-          b[i] = half2_bits(x, y);
-        } else {
-          __nv_bfloat162 hv = __floats2bfloat162_rn(x, y);
-          b[i] = *reinterpret_cast<uint32_t*>(&hv);
-        }
-      }
-      char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
-      if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
-      else *reinterpret_cast<uint32_t*>(p) = b[0];
-      if (a.lse && lane == r) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
+  for (int i = 0; i < V / 2; ++i) {
+    const float x = l == 0.0f ? 0.0f : v[2 * i] * inv, y = l == 0.0f ? 0.0f : v[2 * i + 1] * inv;
+    if (a.dtype == QG_F16) {
+      b[i] = half2_bits(x, y);
+    } else {
+      __nv_bfloat162 hv = __floats2bfloat162_rn(x, y);
+      b[i] = *reinterpret_cast<uint32_t*>(&hv);
     }
   }
+  char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+  else *reinterpret_cast<uint32_t*>(p) = b[0];
+  if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
 }
 
 template <int D, int NT>
-__device__ __forceinline__ void write_part(float* p, int row0, int lane, float top, float l, const float (&v)[8][D / 32]) {
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    if constexpr (D == 128)
-      *reinterpret_cast<float4*>(p + (row0 + r) * D + 4 * lane) = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
-    else
-      *reinterpret_cast<float2*>(p + (row0 + r) * D + 2 * lane) = make_float2(v[r][0], v[r][1]);
-  }
-  if (lane < 8) *reinterpret_cast<float2*>(p + 8 * NT * D + 2 * (row0 + lane)) = make_float2(top, l);
+__device__ __forceinline__ void write_part(float* p, int row, int lane, float top, float l, const float (&v)[D / 32]) {
+  if constexpr (D == 128) *reinterpret_cast<float4*>(p + row * D + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+  else *reinterpret_cast<float2*>(p + row * D + 2 * lane) = make_float2(v[0], v[1]);
+  if (lane == 0) *reinterpret_cast<float2*>(p + 8 * NT * D + 2 * row) = make_float2(top, l);
 }
 
 template <int G, int NT>
-__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
+__global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
     attention_kv4_decode(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch) {
-  constexpr int kWarps = kWarpsOf<NT>;
+  constexpr int kWarps = kWarpsOf<G, NT>;
   constexpr int D = 64 * G;
   constexpr uint32_t kCodes = kChunk * D / 2, kParams = kChunk * G * 4;
   constexpr uint32_t kStage = 2 * (kCodes + kParams);
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
   // a warp's parts: of an item that another worker started (1: goes on behind this worker, 2: ends here), and of
   // one that starts here and goes on
   struct Left {
-    int head, head_b, head_h, tail, tail_b, tail_h, tail_last;
+    int head, head_first, head_n, head_h, tail, tail_first, tail_n, tail_h, tail_last;
   };
   __shared__ Left left[kWarps];
   int* prefix = reinterpret_cast<int*>(smem);  // before the ring is used
@@ -519,10 +526,11 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
                         : scratch.warp_parts + ((int64_t)(blockIdx.x * kWarps + warp) * 2 + starts_item) * part_floats(NT, D);
     if (!whole && lane == 0) {
       if (starts_item)
-        left[warp].tail = 1, left[warp].tail_b = use.b, left[warp].tail_h = use.h,
+        left[warp].tail = 1, left[warp].tail_first = s.first, left[warp].tail_n = s.n, left[warp].tail_h = use.h,
         left[warp].tail_last = u0 + units - 1 + s.chunks - 1 - use.c;
       else
-        left[warp].head = use.c + 1 == s.chunks ? 2 : 1, left[warp].head_b = use.b, left[warp].head_h = use.h;
+        left[warp].head = use.c + 1 == s.chunks ? 2 : 1, left[warp].head_first = s.first, left[warp].head_n = s.n,
+        left[warp].head_h = use.h;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -817,20 +825,22 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
   const int kind = lane < kWarps ? left[lane].head : 0;
   const uint32_t heads = __ballot_sync(0xffffffffu, kind != 0), done = __ballot_sync(0xffffffffu, kind == 2);
   const uint32_t tails = __ballot_sync(0xffffffffu, lane < kWarps && left[lane].tail != 0);
-  // groups: the first warp's head (if it goes on from another CTA), and every tail; group k is warp (k mod warps)'s
+  // groups: the first warp's head (if it goes on from another CTA), and every tail; their rows go round the warps
   const uint32_t starts_at = tails << 1 | (heads & 1);  // bit 0: that head, bit w + 1: warp w's tail
   const int last = 31 - __clz(tails);                   // the only item that can leave the CTA starts here
   const bool crosses = tails != 0 && (done >> (last + 1)) == 0;
   if (tid == 0) {
     Crossing cross = {0, 0, 0, 0};
     if (crosses)
-      cross = {left[last].tail_b, left[last].tail_h, (int)(ctas.taker(left[last].tail_last) - blockIdx.x) + 1, 0};
+      cross = {left[last].tail_first, left[last].tail_n, left[last].tail_h,
+               (int)(ctas.taker(left[last].tail_last) - blockIdx.x) + 1};
     scratch.crossing[blockIdx.x] = cross;
   }
   if (alone) return;
+  int unit = 0;
 #pragma unroll 1
-  for (int k = warp; k <= kWarps; k += kWarps) {
-    if (!(starts_at >> k & 1)) continue;
+  for (uint32_t todo = starts_at; todo; todo &= todo - 1) {
+    const int k = __ffs(todo) - 1;
     const bool starts = k > 0;
     const int w0 = starts ? k - 1 : 0;  // the group's first part is this warp's
     // the heads that follow: up to the first that ends the item, all of them without a gap
@@ -842,58 +852,42 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
       ends = until <= run;
       count += min(run, until);
     }
-    const int b = starts ? left[w0].tail_b : left[w0].head_b, h = starts ? left[w0].tail_h : left[w0].head_h;
-    int first, n, len;
-    attn4_sequence(a, b, first, n, len);
+    const int first = starts ? left[w0].tail_first : left[w0].head_first, h = starts ? left[w0].tail_h : left[w0].head_h;
+    const int rows = (starts ? left[w0].tail_n : left[w0].head_n) * a.group;
 #pragma unroll 1
-    for (int row0 = 0; row0 < n * a.group; row0 += 8) {
-      float v[8][D / 32], top, l;
+    for (int row = (warp + kWarps - unit % kWarps) % kWarps; row < rows; row += kWarps) {
+      float v[D / 32], top, l;
       add_parts<D, NT>(
           [&](int i) { return base + (int64_t)(i == 0 ? 2 * w0 + starts : 2 * (w0 + i)) * part_floats(NT, D); }, count,
-          row0, lane, top, l, v);
-      if (starts && ends) write_rows<D>(a, first, h, row0, n * a.group, lane, top, l, v);
+          row, lane, top, l, v);
+      if (starts && ends) write_row<D>(a, first, h, row, lane, top, l, v);
       else
-        write_part<D, NT>(scratch.cta_parts + (int64_t)(blockIdx.x * 2 + starts) * part_floats(NT, D), row0, lane, top, l, v);
+        write_part<D, NT>(scratch.cta_parts + (int64_t)(blockIdx.x * 2 + starts) * part_floats(NT, D), row, lane, top, l, v);
     }
+    unit += rows;
   }
 }
 
-// Joins the parts of the (sequence, head)s that cross CTAs: block (8 rows, CTA in which it starts), the CTAs' parts
-// in eight strands that are then added in order.
+// Joins the parts of the (sequence, head)s that cross CTAs: block (8 rows, CTA in which it starts), a warp per row.
 template <int D, int NT>
 __global__ void __launch_bounds__(256)
     attention_kv4_join(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch) {
-  __shared__ __align__(16) float strands[8][part_floats(1, D)];
   pdl_trigger();
   pdl_wait();
-  const int row0 = blockIdx.x * 8, cta = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int cta = blockIdx.y, lane = threadIdx.x & 31, row = blockIdx.x * 8 + threadIdx.x / 32;
   const Crossing c = scratch.crossing[cta];
-  if (c.ctas == 0) return;
-  int first, n, len;
-  attn4_sequence(a, c.b, first, n, len);
-  if (row0 >= n * a.group) return;
-  const int each = (c.ctas + 7) / 8, from = warp * each, used = (c.ctas + each - 1) / each;
-  float v[8][D / 32], top, l;
-  if (warp < used) {
-    add_parts<D, NT>(
-        [&](int i) {
-          const int k = from + i;
-          return scratch.cta_parts + (int64_t)((cta + k) * 2 + (k == 0)) * part_floats(NT, D);
-        },
-        min(each, c.ctas - from), row0, lane, top, l, v);
-    write_part<D, 1>(strands[warp], 0, lane, top, l, v);
-  }
-  __syncthreads();
-  if (warp != 0) return;
-  add_parts<D, 1>([&](int i) { return (const float*)strands[i]; }, used, 0, lane, top, l, v);
-  write_rows<D>(a, first, c.h, row0, n * a.group, lane, top, l, v);
+  if (c.ctas == 0 || row >= c.n * a.group) return;
+  float v[D / 32], top, l;
+  add_parts<D, NT>([&](int k) { return scratch.cta_parts + (int64_t)((cta + k) * 2 + (k == 0)) * part_floats(NT, D); },
+                   c.ctas, row, lane, top, l, v);
+  write_row<D>(a, c.first, c.h, row, lane, top, l, v);
 }
 
 size_t crossing_bytes() { return (size_t)sm_count() * sizeof(Crossing); }
 
 template <int G, int NT>
 qg_status launch(const Attn4& a, void* workspace, cudaStream_t s) {
-  constexpr int D = 64 * G, kWarps = kWarpsOf<NT>;
+  constexpr int D = 64 * G, kWarps = kWarpsOf<G, NT>;
   constexpr int kRing = kWarps * kStages * 2 * kChunk * (D / 2 + 4 * G);
   constexpr int kMost = kRing > 4097 * 4 ? kRing : 4097 * 4;  // the prefix of 4096 sequences shares the ring's place
   static PerDeviceOnce once;
@@ -919,7 +913,7 @@ qg_status launch(const Attn4& a, void* workspace, cudaStream_t s) {
 }  // namespace
 
 size_t attention_kv4_decode_workspace(int64_t dim, int nt) {
-  return crossing_bytes() + (size_t)sm_count() * ((nt == 1 ? kWarpsOf<1> : kWarpsOf<2>) + 1) * 2 * part_floats(nt, (int)dim) * sizeof(float);
+  return crossing_bytes() + (size_t)sm_count() * ((nt == 2 ? kWarpsOf<2, 2> : dim == 64 ? kWarpsOf<1, 1> : kWarpsOf<2, 1>) + 1) * 2 * part_floats(nt, (int)dim) * sizeof(float);
 }
 
 qg_status launch_attention_kv4_decode(const Attn4& a, int nt, void* workspace, cudaStream_t s) {
