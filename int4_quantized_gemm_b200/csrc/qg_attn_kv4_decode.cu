@@ -293,7 +293,7 @@ __device__ __forceinline__ void write_part(float* p, int row, int lane, float to
 
 template <int G, int NT>
 __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
-    attention_kv4_decode(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch) {
+    attention_kv4_decode(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch, bool behind_prompts) {
   constexpr int kWarps = kWarpsOf<G, NT>;
   constexpr int D = 64 * G;
   constexpr uint32_t kCodes = kChunk * D / 2, kParams = kChunk * G * 4;
@@ -317,7 +317,11 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
     fence_mbar_init();
   }
   pdl_trigger();
-  pdl_wait();
+  // Behind the prompt kernel of the same call this one works on the blocks' place as they leave: that kernel lets its
+  // dependents start once all of its blocks are past their own wait, and shares no output with this one.  The last
+  // block waits for it instead, so that what follows waits for both.
+  if (!behind_prompts) pdl_wait();
+  else __threadfence();
 
   // prefix[b]: chunks (times heads) of the sequences before b
   const int per = (a.B + 32 * kWarps - 1) / (32 * kWarps);
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
     if (copies && t < fill.s.len) {
       const int i = (int)kv4_page(a.cache, (uint32_t)t >> 4);  // t / P
       in_page = t - i * P;
-      page = __ldg(a.table + (int64_t)fill.b * a.table_ld + i);
+      page = a.table[(int64_t)fill.b * a.table_ld + i];
       if (page < 0 || page >= a.cache.pages) {
         report(kDevBadArg, kSitePage);
         page = -1;
@@ -816,6 +820,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
     if (i + 1 < units) use.next(a);
   }
 
+  if (behind_prompts && blockIdx.x == gridDim.x - 1) pdl_wait();
   // --- what the warps left unfinished -----------------------------------------
   // In list order: each warp's continued item, then the one it started.  A group of parts that belong together
   // begins with a started item (or the CTA's first part) and takes every continued one up to the item's end.
@@ -886,7 +891,16 @@ __global__ void __launch_bounds__(256)
 size_t crossing_bytes() { return (size_t)sm_count() * sizeof(Crossing); }
 
 template <int G, int NT>
-qg_status launch(const Attn4& a, void* workspace, cudaStream_t s) {
+Scratch scratch_of(void* workspace) {
+  Scratch s;
+  s.crossing = static_cast<Crossing*>(workspace);
+  s.warp_parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + crossing_bytes());
+  s.cta_parts = s.warp_parts + (int64_t)sm_count() * kWarpsOf<G, NT> * 2 * part_floats(NT, 64 * G);
+  return s;
+}
+
+template <int G, int NT>
+qg_status launch(const Attn4& a, bool behind_prompts, void* workspace, cudaStream_t s) {
   constexpr int D = 64 * G, kWarps = kWarpsOf<G, NT>;
   constexpr int kRing = kWarps * kStages * 2 * kChunk * (D / 2 + 4 * G);
   constexpr int kMost = kRing > 4097 * 4 ? kRing : 4097 * 4;  // the prefix of 4096 sequences shares the ring's place
@@ -897,17 +911,18 @@ qg_status launch(const Attn4& a, void* workspace, cudaStream_t s) {
   });
   if (st != QG_OK) return st;
   const int grid = sm_count();
-  Scratch scratch;
-  scratch.crossing = static_cast<Crossing*>(workspace);
-  scratch.warp_parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + crossing_bytes());
-  scratch.cta_parts = scratch.warp_parts + (int64_t)grid * kWarps * 2 * part_floats(NT, D);
+  const Scratch scratch = scratch_of<G, NT>(workspace);
   LaunchCfg lc((unsigned)grid, 32 * kWarps, kMost, s);
-  cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_decode<G, NT>, a, scratch);
-  if (e != cudaSuccess) return check_cuda(e, "attention_kv4 decode launch");
-  LaunchCfg lj(NT, 256, 0, s);
-  lj.cfg.gridDim.y = (unsigned)grid;
-  e = cudaLaunchKernelEx(&lj.cfg, attention_kv4_join<D, NT>, a, scratch);
-  return check_cuda(e, "attention_kv4 join launch");
+  cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_decode<G, NT>, a, scratch, behind_prompts);
+  return check_cuda(e, "attention_kv4 decode launch");
+}
+
+template <int G, int NT>
+qg_status launch_join(const Attn4& a, void* workspace, cudaStream_t s) {
+  const Scratch scratch = scratch_of<G, NT>(workspace);
+  LaunchCfg lc(NT, 256, 0, s);
+  lc.cfg.gridDim.y = (unsigned)sm_count();
+  return check_cuda(cudaLaunchKernelEx(&lc.cfg, attention_kv4_join<64 * G, NT>, a, scratch), "attention_kv4 join launch");
 }
 
 }  // namespace
@@ -916,9 +931,15 @@ size_t attention_kv4_decode_workspace(int64_t dim, int nt) {
   return crossing_bytes() + (size_t)sm_count() * ((nt == 2 ? kWarpsOf<2, 2> : dim == 64 ? kWarpsOf<1, 1> : kWarpsOf<2, 1>) + 1) * 2 * part_floats(nt, (int)dim) * sizeof(float);
 }
 
-qg_status launch_attention_kv4_decode(const Attn4& a, int nt, void* workspace, cudaStream_t s) {
-  if (a.cache.dim == 64) return nt == 1 ? launch<1, 1>(a, workspace, s) : launch<1, 2>(a, workspace, s);
-  return nt == 1 ? launch<2, 1>(a, workspace, s) : launch<2, 2>(a, workspace, s);
+qg_status launch_attention_kv4_decode(const Attn4& a, int nt, bool behind_prompts, void* workspace, cudaStream_t s) {
+  if (a.cache.dim == 64)
+    return nt == 1 ? launch<1, 1>(a, behind_prompts, workspace, s) : launch<1, 2>(a, behind_prompts, workspace, s);
+  return nt == 1 ? launch<2, 1>(a, behind_prompts, workspace, s) : launch<2, 2>(a, behind_prompts, workspace, s);
+}
+
+qg_status launch_attention_kv4_decode_join(const Attn4& a, int nt, void* workspace, cudaStream_t s) {
+  if (a.cache.dim == 64) return nt == 1 ? launch_join<1, 1>(a, workspace, s) : launch_join<1, 2>(a, workspace, s);
+  return nt == 1 ? launch_join<2, 1>(a, workspace, s) : launch_join<2, 2>(a, workspace, s);
 }
 
 }  // namespace qg

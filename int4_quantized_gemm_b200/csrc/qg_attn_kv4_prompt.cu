@@ -326,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&drained), 2);
     fence_mbar_init();
   }
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // behind the wait: the decode kernel of a ragged call relies on it
   if (blockIdx.x == 0)
     for (int b = tid; b < a.B; b += kThreads) {
       int f, n, l;
@@ -851,6 +851,16 @@ int key_splits(int64_t tiles, int64_t heads) {
 }
 
 template <int G>
+Parts<G> parts_of(const Attn4& a, int splits, void* workspace) {
+  Parts<G> p = {};
+  if (splits > 1) {
+    p.sums = static_cast<float*>(workspace);
+    p.ml = reinterpret_cast<float2*>(p.sums + (int64_t)splits * a.T * a.heads_q * 64 * G);
+  }
+  return p;
+}
+
+template <int G>
 qg_status launch(const Attn4& a, int min_rows, void* workspace, cudaStream_t s) {
   constexpr int kSmem = Layout<G>::bytes + 1024;
   static PerDeviceOnce once;
@@ -867,18 +877,21 @@ qg_status launch(const Attn4& a, int min_rows, void* workspace, cudaStream_t s) 
   const int64_t tiles = row_tiles(a.B, a.T, a.group, a.q_starts != nullptr);
   const int splits = key_splits(tiles, a.cache.heads);
   if (tiles * a.cache.heads * splits >= ((int64_t)1 << 31)) return fail(QG_ERR_UNSUPPORTED, "attention_kv4: too many row tiles");
-  Parts<G> parts = {};
-  if (splits > 1) {
-    parts.sums = static_cast<float*>(workspace);
-    parts.ml = reinterpret_cast<float2*>(parts.sums + (int64_t)splits * a.T * a.heads_q * 64 * G);
-  }
+  const Parts<G> parts = parts_of<G>(a, splits, workspace);
   LaunchCfg lc((unsigned)(tiles * a.cache.heads * splits), kThreads, kSmem, s);
-  cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt<G>, a, min_rows, splits, parts);
-  if (e != cudaSuccess || splits == 1) return check_cuda(e, "attention_kv4 prompt launch");
-  LaunchCfg lj((unsigned)(tiles * a.cache.heads), 256, 0, s);
-  lj.cfg.gridDim.y = kRows / 32;
-  e = cudaLaunchKernelEx(&lj.cfg, attention_kv4_prompt_join<G>, a, min_rows, splits, parts);
-  return check_cuda(e, "attention_kv4 prompt join launch");
+  const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt<G>, a, min_rows, splits, parts);
+  return check_cuda(e, "attention_kv4 prompt launch");
+}
+
+template <int G>
+qg_status launch_join(const Attn4& a, int min_rows, void* workspace, cudaStream_t s) {
+  const int64_t tiles = row_tiles(a.B, a.T, a.group, a.q_starts != nullptr);
+  const int splits = key_splits(tiles, a.cache.heads);
+  if (splits == 1) return QG_OK;
+  LaunchCfg lc((unsigned)(tiles * a.cache.heads), 256, 0, s);
+  lc.cfg.gridDim.y = kRows / 32;
+  return check_cuda(cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt_join<G>, a, min_rows, splits, parts_of<G>(a, splits, workspace)),
+                    "attention_kv4 prompt join launch");
 }
 
 // Rows (query tokens x head group) that the decode kernel takes, in tiles of 8; 0: none.  A ragged call gives it
@@ -903,16 +916,21 @@ size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t he
   return bytes;
 }
 
-// Single tokens and drafts go to the decode kernel, longer ones here; a ragged
-// call launches both and each takes its sequences.
+// Single tokens and drafts go to the decode kernel, longer ones here; a ragged call launches both and each takes its
+// sequences: first the prompts, then the others on the place that their blocks leave.
 qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s) {
   const int nt = decode_tiles(a.n_uniform, a.group, a.q_starts != nullptr);
-  if (nt) {
-    const qg_status st = launch_attention_kv4_decode(a, nt, workspace, s);
-    if (st != QG_OK || !a.q_starts) return st;
-    workspace = static_cast<char*>(workspace) + round256(attention_kv4_decode_workspace(a.cache.dim, nt));
-  }
-  return a.cache.dim == 64 ? launch<1>(a, 8 * nt + 1, workspace, s) : launch<2>(a, 8 * nt + 1, workspace, s);
+  const bool prompts = !nt || a.q_starts;
+  const auto run = [&](auto&& f1, auto&& f2) { return a.cache.dim == 64 ? f1() : f2(); };
+  void* const mine = static_cast<char*>(workspace) + (nt ? round256(attention_kv4_decode_workspace(a.cache.dim, nt)) : 0);
+  qg_status st = QG_OK;
+  if (prompts)
+    st = run([&] { return launch<1>(a, 8 * nt + 1, mine, s); }, [&] { return launch<2>(a, 8 * nt + 1, mine, s); });
+  if (st == QG_OK && nt) st = launch_attention_kv4_decode(a, nt, prompts, workspace, s);
+  if (st == QG_OK && prompts)
+    st = run([&] { return launch_join<1>(a, 8 * nt + 1, mine, s); }, [&] { return launch_join<2>(a, 8 * nt + 1, mine, s); });
+  if (st == QG_OK && nt) st = launch_attention_kv4_decode_join(a, nt, workspace, s);
+  return st;
 }
 
 }  // namespace qg
