@@ -169,11 +169,34 @@ __device__ __forceinline__ bool not_finite(uint32_t p) {
 }
 
 struct Job {
-  int b, h, tile, split;      // sequence, KV head, 256-row tile, share of the keys
+  int b, h, tile;             // sequence, KV head, 256-row tile
+  int split;                  // share of the keys
   int first, n, len, rows;    // the sequence
 };
 
-// Which rows a block works on; tiles in descending order, so that a causal mask's longest start first.
+// Shares of the keys: as many as there are SMs for the (row tile, head)s, at most 32.
+__host__ __device__ __forceinline__ int key_splits(int64_t tiles, int64_t heads, int sms) {
+  const int64_t n = sms / (tiles * heads > 1 ? tiles * heads : 1);
+  return n < 1 ? 1 : n > 32 ? 32 : (int)n;
+}
+
+__device__ __forceinline__ int tiles_of(const Attn4& a, int b, int min_rows) {
+  int first, n, len;
+  attn4_sequence(a, b, first, n, len);
+  return n * a.group >= min_rows ? (n * a.group + kRows - 1) / kRows : 0;
+}
+
+// The shares of the keys of each of the call's tiles: the row counts of a ragged call are on the device.
+__device__ __forceinline__ int splits_of(const Attn4& a, int min_rows, int sms, int lane) {
+  if (!a.q_starts) return key_splits((int64_t)a.B * ((a.n_uniform * a.group + kRows - 1) / kRows), a.cache.heads, sms);
+  int tiles = 0;
+#pragma unroll 4
+  for (int b = lane; b < a.B; b += 32) tiles += tiles_of(a, b, min_rows);
+  return key_splits(__reduce_add_sync(0xffffffffu, tiles), a.cache.heads, sms);
+}
+
+// Which rows a block works on, in blocks of (tile, split, head); a sequence's tiles in descending order, so that a
+// causal mask's longest start first.
 __device__ __forceinline__ bool find_job(const Attn4& a, int min_rows, int splits, int block, int lane, Job& j) {
   j.h = block % a.cache.heads;
   block /= a.cache.heads;
@@ -188,11 +211,7 @@ __device__ __forceinline__ bool find_job(const Attn4& a, int min_rows, int split
     int base = 0, at = 0;
     j.b = -1;
     for (; base < a.B; base += 32) {  // the whole warp
-      int first, n = 0, len, tiles = 0;
-      if (base + lane < a.B) {
-        attn4_sequence(a, base + lane, first, n, len);
-        if (n * a.group >= min_rows) tiles = (n * a.group + kRows - 1) / kRows;
-      }
+      const int tiles = base + lane < a.B ? tiles_of(a, base + lane, min_rows) : 0;
       int scan = tiles;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -287,16 +306,16 @@ __device__ __forceinline__ float row_exp(const uint32_t (&v)[2][32], uint32_t ts
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// A part of a row for the join: D sums, then (log2 maximum, sum).
+// Parts of rows for the join, of each block's 256 rows: D sums, and (log2 maximum, sum).
 template <int G>
 struct Parts {
-  float* sums;  // [splits][T heads_q][D]
-  float2* ml;   // [splits][T heads_q]
+  float* sums;  // [blocks][256][D]
+  float2* ml;   // [blocks][256]
 };
 
-template <int G>
+template <int G, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
-    attention_kv4_prompt(const __grid_constant__ Attn4 a, int min_rows, int splits, const Parts<G> parts) {
+    attention_kv4_prompt(const __grid_constant__ Attn4 a, int min_rows, int sms, const Parts<G> parts) {
   using L = Layout<G>;
   constexpr int D = L::D;
   extern __shared__ uint8_t smem_raw[];
@@ -334,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!attn4_sequence(a, b, f, n, l)) report(kDevBadArg, kSiteSequence);
     }
   Job job;
+  const int splits = kSplit ? splits_of(a, min_rows, sms, lane) : 1;
   if (!find_job(a, min_rows, splits, blockIdx.x, lane, job)) return;  // the same for every warp
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&tmem_slot), 512);
@@ -717,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait(smem_u32(&o_done[tile][j & 1]), j >> 1 & 1, &g_status_prompt, kSiteO);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    const int64_t flat = (int64_t)job.split * a.T * a.heads_q + (int64_t)t_row * a.heads_q + hq;
+    const int64_t flat = (int64_t)blockIdx.x * kRows + tile * 128 + wrow + lane;  // of the parts
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const uint32_t my_row = sm + L::q + tile * L::kOperand + (wrow + lane) * 128;  // the queries have been read
 #pragma unroll
@@ -791,19 +811,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the splits' parts: block (tile, head) as above, a warp per row.
 template <int G>
 __global__ void __launch_bounds__(256)
-    attention_kv4_prompt_join(const __grid_constant__ Attn4 a, int min_rows, int splits, const Parts<G> parts) {
+    attention_kv4_prompt_join(const __grid_constant__ Attn4 a, int min_rows, int sms, const Parts<G> parts) {
   constexpr int D = 64 * G, V = D / 32;
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   Job job;
-  if (!find_job(a, min_rows, 1, blockIdx.x, lane, job)) return;
-  const int64_t stride = (int64_t)a.T * a.heads_q;
+  const int splits = splits_of(a, min_rows, sms, lane);
+  if (splits == 1 || !find_job(a, min_rows, 1, blockIdx.x, lane, job)) return;
+  const int64_t stride = (int64_t)a.cache.heads * kRows;  // a split further
   const int row0 = job.tile * kRows + blockIdx.y * 32;
 #pragma unroll 1
   for (int row = row0 + warp; row < min(row0 + 32, job.rows); row += 8) {
     const int t = job.first + row / a.group, hq = job.h * a.group + row % a.group;
-    const int64_t flat = (int64_t)t * a.heads_q + hq;
+    const int64_t flat = ((int64_t)(blockIdx.x / a.cache.heads * splits) * a.cache.heads + job.h) * kRows + row - job.tile * kRows;
     float top = -INFINITY, l = 0.0f, v[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) v[k] = 0.0f;
@@ -836,7 +857,7 @@ __global__ void __launch_bounds__(256)
     char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
     if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
     else *reinterpret_cast<uint32_t*>(p) = b[0];
-    if (a.lse && lane == 0) a.lse[flat] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
+    if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
   }
 }
 
@@ -845,60 +866,64 @@ int64_t row_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
   return ragged ? T * group / kRows + B : B * ((T / B * group + kRows - 1) / kRows);
 }
 
-// Shares of the keys: as many as there are SMs for the (row tile, head)s, at most 32.
-int key_splits(int64_t tiles, int64_t heads) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(32, sm_count() / std::max<int64_t>(1, tiles * heads)));
-}
-
-template <int G>
-Parts<G> parts_of(const Attn4& a, int splits, void* workspace) {
-  Parts<G> p = {};
-  if (splits > 1) {
-    p.sums = static_cast<float*>(workspace);
-    p.ml = reinterpret_cast<float2*>(p.sums + (int64_t)splits * a.T * a.heads_q * 64 * G);
-  }
-  return p;
-}
-
-template <int G>
-qg_status launch(const Attn4& a, int min_rows, void* workspace, cudaStream_t s) {
-  constexpr int kSmem = Layout<G>::bytes + 1024;
-  static PerDeviceOnce once;
-  const qg_status st = once.run([](int) {
-    // the warps' register shares are drawn on the block's own: fewer at launch would wait for ever
-    cudaFuncAttributes f;
-    const qg_status q = check_cuda(cudaFuncGetAttributes(&f, attention_kv4_prompt<G>), "attention_kv4 attributes");
-    if (q != QG_OK) return q;
-    if (f.numRegs < kLaunchRegs) return fail(QG_ERR_UNSUPPORTED, "attention_kv4: built with %d registers a thread, %d needed", f.numRegs, kLaunchRegs);
-    return check_cuda(cudaFuncSetAttribute(attention_kv4_prompt<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-                      "attention_kv4 shared memory");
-  });
-  if (st != QG_OK) return st;
-  const int64_t tiles = row_tiles(a.B, a.T, a.group, a.q_starts != nullptr);
-  const int splits = key_splits(tiles, a.cache.heads);
-  if (tiles * a.cache.heads * splits >= ((int64_t)1 << 31)) return fail(QG_ERR_UNSUPPORTED, "attention_kv4: too many row tiles");
-  const Parts<G> parts = parts_of<G>(a, splits, workspace);
-  LaunchCfg lc((unsigned)(tiles * a.cache.heads * splits), kThreads, kSmem, s);
-  const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt<G>, a, min_rows, splits, parts);
-  return check_cuda(e, "attention_kv4 prompt launch");
-}
-
-template <int G>
-qg_status launch_join(const Attn4& a, int min_rows, void* workspace, cudaStream_t s) {
-  const int64_t tiles = row_tiles(a.B, a.T, a.group, a.q_starts != nullptr);
-  const int splits = key_splits(tiles, a.cache.heads);
-  if (splits == 1) return QG_OK;
-  LaunchCfg lc((unsigned)(tiles * a.cache.heads), 256, 0, s);
-  lc.cfg.gridDim.y = kRows / 32;
-  return check_cuda(cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt_join<G>, a, min_rows, splits, parts_of<G>(a, splits, workspace)),
-                    "attention_kv4 prompt join launch");
-}
-
 // Rows (query tokens x head group) that the decode kernel takes, in tiles of 8; 0: none.  A ragged call gives it
 // the sequences of 8 rows at most (16 where one token has more than 8).
 int decode_tiles(int64_t n, int64_t group, bool ragged) {
   const int64_t rows = ragged ? group : n * group;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
+}
+
+// Blocks of a call, and those that leave parts (0: every tile's keys are one share, and the kernel without parts takes
+// them, 340 instead of 353 us for 2 x 4096 tokens of 32 heads).  The device counts a ragged call's tiles, but the query
+// tokens that its sequences share make a least number of them, with which nothing is split.
+struct Blocks {
+  int64_t all, parts;
+};
+Blocks blocks_of(int64_t B, int64_t T, int64_t group, int64_t heads, bool ragged, int nt) {
+  const int64_t items = row_tiles(B, T, group, ragged) * heads;
+  if (ragged) {
+    const int64_t rows = T * group - B * 8 * nt, least = rows > 0 ? (rows + kRows - 1) / kRows * heads : 0;
+    if (2 * least > sm_count()) return {items, 0};
+    return {std::max<int64_t>(items, sm_count()), sm_count()};  // tiles x heads x splits: the SMs at most
+  }
+  const int splits = key_splits(items, 1, sm_count());
+  return {items * splits, splits > 1 ? items * splits : 0};
+}
+
+template <int G>
+Parts<G> parts_of(int64_t blocks, void* workspace) {
+  Parts<G> p;
+  p.sums = static_cast<float*>(workspace);
+  p.ml = reinterpret_cast<float2*>(p.sums + blocks * kRows * 64 * G);
+  return p;
+}
+
+template <int G, bool kSplit>
+qg_status launch(const Attn4& a, int min_rows, const Blocks& n, void* workspace, cudaStream_t s) {
+  constexpr int kSmem = Layout<G>::bytes + 1024;
+  static PerDeviceOnce once;
+  const qg_status st = once.run([](int) {
+    // the warps' register shares are drawn on the block's own: fewer at launch would wait for ever
+    cudaFuncAttributes f;
+    const qg_status q = check_cuda(cudaFuncGetAttributes(&f, attention_kv4_prompt<G, kSplit>), "attention_kv4 attributes");
+    if (q != QG_OK) return q;
+    if (f.numRegs < kLaunchRegs) return fail(QG_ERR_UNSUPPORTED, "attention_kv4: built with %d registers a thread, %d needed", f.numRegs, kLaunchRegs);
+    return check_cuda(cudaFuncSetAttribute(attention_kv4_prompt<G, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+                      "attention_kv4 shared memory");
+  });
+  if (st != QG_OK) return st;
+  if (n.all >= ((int64_t)1 << 31)) return fail(QG_ERR_UNSUPPORTED, "attention_kv4: too many row tiles");
+  LaunchCfg lc((unsigned)n.all, kThreads, kSmem, s);
+  return check_cuda(cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt<G, kSplit>, a, min_rows, sm_count(), parts_of<G>(n.parts, workspace)),
+                    "attention_kv4 prompt launch");
+}
+
+template <int G>
+qg_status launch_join(const Attn4& a, int min_rows, const Blocks& n, void* workspace, cudaStream_t s) {
+  LaunchCfg lc((unsigned)(n.parts / 2), 256, 0, s);  // two splits or more each
+  lc.cfg.gridDim.y = kRows / 32;
+  return check_cuda(cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt_join<G>, a, min_rows, sm_count(), parts_of<G>(n.parts, workspace)),
+                    "attention_kv4 prompt join launch");
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -910,8 +935,7 @@ size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t he
   const int nt = decode_tiles(T / B, group, ragged);
   size_t bytes = nt ? round256(attention_kv4_decode_workspace(dim, nt)) : 0;
   if (!nt || ragged) {
-    const int splits = key_splits(row_tiles(B, T, group, ragged), heads);
-    if (splits > 1) bytes += (size_t)splits * T * heads_q * (dim + 2) * sizeof(float);
+    bytes += (size_t)blocks_of(B, T, group, heads, ragged, nt).parts * kRows * (dim + 2) * sizeof(float);
   }
   return bytes;
 }
@@ -921,14 +945,17 @@ size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t he
 qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s) {
   const int nt = decode_tiles(a.n_uniform, a.group, a.q_starts != nullptr);
   const bool prompts = !nt || a.q_starts;
-  const auto run = [&](auto&& f1, auto&& f2) { return a.cache.dim == 64 ? f1() : f2(); };
+  const Blocks n = blocks_of(a.B, a.T, a.group, a.cache.heads, a.q_starts != nullptr, nt);
+  const int min_rows = 8 * nt + 1;
   void* const mine = static_cast<char*>(workspace) + (nt ? round256(attention_kv4_decode_workspace(a.cache.dim, nt)) : 0);
   qg_status st = QG_OK;
-  if (prompts)
-    st = run([&] { return launch<1>(a, 8 * nt + 1, mine, s); }, [&] { return launch<2>(a, 8 * nt + 1, mine, s); });
+  if (prompts && a.cache.dim == 64)
+    st = n.parts ? launch<1, true>(a, min_rows, n, mine, s) : launch<1, false>(a, min_rows, n, mine, s);
+  else if (prompts)
+    st = n.parts ? launch<2, true>(a, min_rows, n, mine, s) : launch<2, false>(a, min_rows, n, mine, s);
   if (st == QG_OK && nt) st = launch_attention_kv4_decode(a, nt, prompts, workspace, s);
-  if (st == QG_OK && prompts)
-    st = run([&] { return launch_join<1>(a, 8 * nt + 1, mine, s); }, [&] { return launch_join<2>(a, 8 * nt + 1, mine, s); });
+  if (st == QG_OK && prompts && n.parts)
+    st = a.cache.dim == 64 ? launch_join<1>(a, min_rows, n, mine, s) : launch_join<2>(a, min_rows, n, mine, s);
   if (st == QG_OK && nt) st = launch_attention_kv4_decode_join(a, nt, workspace, s);
   return st;
 }
