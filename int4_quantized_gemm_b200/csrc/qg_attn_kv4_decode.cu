@@ -45,7 +45,7 @@
 
 #include "qg_device.cuh"
 #include "qg_internal.h"
-#include "qg_kv4.cuh"
+#include "qg_kv4_join.cuh"
 
 namespace qg {
 
@@ -78,12 +78,6 @@ __device__ __forceinline__ void report(uint32_t code, uint32_t site) {
             (unsigned long long)code | ((unsigned long long)site << 8) | ((unsigned long long)blockIdx.x << 24));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm(
@@ -112,11 +106,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
 }
 
 __device__ __forceinline__ float2 half2_f32(uint32_t v) {
@@ -203,85 +192,9 @@ struct Scratch {
   float* cta_parts;    // [grid][2]
 };
 
-// Adds `count` parts (part(i), i = 0, 1, ...) of a row, a warp: its log2 maximum and sum, and V values in each lane.
-// The parts' weights first, a lane each; no load waits for another part's.
-template <int D, int NT, class F>
-__device__ __forceinline__ void add_parts(F part, int count, int row, int lane, float& top, float& l,
-                                          float (&v)[D / 32]) {
-  constexpr int V = D / 32, kBatch = 8;
-  top = -INFINITY;
-  l = 0.0f;
-#pragma unroll
-  for (int k = 0; k < V; ++k) v[k] = 0.0f;
-#pragma unroll 1
-  for (int i0 = 0; i0 < count; i0 += 32) {
-    const int n = min(32, count - i0);
-    float x[kBatch][V];
-    const auto load = [&](int i) {
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) x[b][k] = 0.0f;
-        if (i + b < n) {
-          const float* p = part(i0 + i + b) + row * D + V * lane;
-          if constexpr (V == 4) *reinterpret_cast<float4*>(x[b]) = *reinterpret_cast<const float4*>(p);
-          else *reinterpret_cast<float2*>(x[b]) = *reinterpret_cast<const float2*>(p);
-        }
-      }
-    };
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (lane < n) ml = *reinterpret_cast<const float2*>(part(i0 + lane) + 8 * NT * D + 2 * row);
-    load(0);
-    float t = ml.x;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-    t = fmaxf(t, top);
-    const float safe = t == -INFINITY ? 0.0f : t;
-    const float f = ex2(top - safe), g = ex2(ml.x - safe);
-    float sum = ml.y * g;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    l = fmaf(l, f, sum);
-    top = t;
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] *= f;
-#pragma unroll 1
-    for (int i = 0;;) {
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const float gb = __shfl_sync(0xffffffffu, g, (i + b) & 31);
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = fmaf(x[b][k], i + b < n ? gb : 0.0f, v[k]);
-      }
-      i += kBatch;
-      if (i >= n) break;
-      load(i);
-    }
-  }
-}
-
-// out (and lse) of a row of an item from its sums, a warp
-template <int D>
-__device__ __forceinline__ void write_row(const Attn4& a, int first, int h, int row, int lane, float top, float l,
-                                          const float (&v)[D / 32]) {
-  constexpr int V = D / 32;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int t = first + row / a.group, hq = h * a.group + row % a.group;
-  uint32_t b[V / 2];
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    const float x = l == 0.0f ? 0.0f : v[2 * i] * inv, y = l == 0.0f ? 0.0f : v[2 * i + 1] * inv;
-    if (a.dtype == QG_F16) {
-      b[i] = half2_bits(x, y);
-    } else {
-      __nv_bfloat162 hv = __floats2bfloat162_rn(x, y);
-      b[i] = *reinterpret_cast<uint32_t*>(&hv);
-    }
-  }
-  char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
-  if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
-  else *reinterpret_cast<uint32_t*>(p) = b[0];
-  if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
+template <int D, int NT>
+__device__ __forceinline__ const float2* part_head(const float* p, int row) {
+  return reinterpret_cast<const float2*>(p + 8 * NT * D + 2 * row);
 }
 
 template <int D, int NT>
@@ -862,9 +775,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
 #pragma unroll 1
     for (int row = (warp + kWarps - unit % kWarps) % kWarps; row < rows; row += kWarps) {
       float v[D / 32], top, l;
-      add_parts<D, NT>(
-          [&](int i) { return base + (int64_t)(i == 0 ? 2 * w0 + starts : 2 * (w0 + i)) * part_floats(NT, D); }, count,
-          row, lane, top, l, v);
+      const auto part = [&](int i) { return base + (int64_t)(i == 0 ? 2 * w0 + starts : 2 * (w0 + i)) * part_floats(NT, D); };
+      add_parts<D>([&](int i) { return part(i) + row * D; }, [&](int i) { return part_head<D, NT>(part(i), row); }, count,
+                   lane, top, l, v);
       if (starts && ends) write_row<D>(a, first, h, row, lane, top, l, v);
       else
         write_part<D, NT>(scratch.cta_parts + (int64_t)(blockIdx.x * 2 + starts) * part_floats(NT, D), row, lane, top, l, v);
@@ -883,8 +796,9 @@ __global__ void __launch_bounds__(256)
   const Crossing c = scratch.crossing[cta];
   if (c.ctas == 0 || row >= c.n * a.group) return;
   float v[D / 32], top, l;
-  add_parts<D, NT>([&](int k) { return scratch.cta_parts + (int64_t)((cta + k) * 2 + (k == 0)) * part_floats(NT, D); },
-                   c.ctas, row, lane, top, l, v);
+  const auto part = [&](int k) { return scratch.cta_parts + (int64_t)((cta + k) * 2 + (k == 0)) * part_floats(NT, D); };
+  add_parts<D>([&](int k) { return part(k) + row * D; }, [&](int k) { return part_head<D, NT>(part(k), row); }, c.ctas, lane,
+               top, l, v);
   write_row<D>(a, c.first, c.h, row, lane, top, l, v);
 }
 

@@ -35,7 +35,7 @@
 
 #include "qg_device.cuh"
 #include "qg_internal.h"
-#include "qg_kv4.cuh"
+#include "qg_kv4_join.cuh"
 
 namespace qg {
 
@@ -75,16 +75,6 @@ __device__ __forceinline__ void report(uint32_t code, uint32_t site) {
             (unsigned long long)code | ((unsigned long long)site << 8) | ((unsigned long long)blockIdx.x << 24));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -808,11 +798,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the splits' parts: block (tile, head) as above, a warp per row.
+// Joins the splits' parts: block (tile, head; 16 rows), a warp per row.
+constexpr int kJoinRows = 16;
 template <int G>
 __global__ void __launch_bounds__(256)
     attention_kv4_prompt_join(const __grid_constant__ Attn4 a, int min_rows, int sms, const Parts<G> parts) {
-  constexpr int D = 64 * G, V = D / 32;
+  constexpr int D = 64 * G;
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -820,44 +811,13 @@ __global__ void __launch_bounds__(256)
   const int splits = splits_of(a, min_rows, sms, lane);
   if (splits == 1 || !find_job(a, min_rows, 1, blockIdx.x, lane, job)) return;
   const int64_t stride = (int64_t)a.cache.heads * kRows;  // a split further
-  const int row0 = job.tile * kRows + blockIdx.y * 32;
+  const int64_t from = ((int64_t)(blockIdx.x / a.cache.heads * splits) * a.cache.heads + job.h) * kRows;
 #pragma unroll 1
-  for (int row = row0 + warp; row < min(row0 + 32, job.rows); row += 8) {
-    const int t = job.first + row / a.group, hq = job.h * a.group + row % a.group;
-    const int64_t flat = ((int64_t)(blockIdx.x / a.cache.heads * splits) * a.cache.heads + job.h) * kRows + row - job.tile * kRows;
-    float top = -INFINITY, l = 0.0f, v[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < splits; ++i) {
-      const float2 ml = parts.ml[flat + i * stride];
-      float x[V];
-      const float* p = parts.sums + (flat + i * stride) * D + V * lane;
-      if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p);
-      else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p);
-      const float tn = fmaxf(top, ml.x), safe = tn == -INFINITY ? 0.0f : tn;
-      const float f = ex2(top - safe), g = ex2(ml.x - safe);
-      l = l * f + ml.y * g;
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = fmaf(x[k], g, v[k] * f);
-      top = tn;
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint32_t b[V / 2];
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const float x = l == 0.0f ? 0.0f : v[2 * i] * inv, y = l == 0.0f ? 0.0f : v[2 * i + 1] * inv;
-      if (a.dtype == QG_F16) {
-        b[i] = half2_bits(x, y);
-      } else {
-        __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        b[i] = *reinterpret_cast<uint32_t*>(&h);
-      }
-    }
-    char* p = static_cast<char*>(a.out) + 2 * (t * a.o_st + hq * a.o_sh + V * lane);
-    if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
-    else *reinterpret_cast<uint32_t*>(p) = b[0];
-    if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads_q + hq] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718056f;
+  for (int r = blockIdx.y * kJoinRows + warp; r < min((int)(blockIdx.y + 1) * kJoinRows, job.rows - job.tile * kRows); r += 8) {
+    float v[D / 32], top, l;
+    add_parts<D>([&](int i) { return parts.sums + (from + r + i * stride) * D; },
+                 [&](int i) { return parts.ml + from + r + i * stride; }, splits, lane, top, l, v);
+    write_row<D>(a, job.first, job.h, job.tile * kRows + r, lane, top, l, v);
   }
 }
 
@@ -921,7 +881,7 @@ qg_status launch(const Attn4& a, int min_rows, const Blocks& n, void* workspace,
 template <int G>
 qg_status launch_join(const Attn4& a, int min_rows, const Blocks& n, void* workspace, cudaStream_t s) {
   LaunchCfg lc((unsigned)(n.parts / 2), 256, 0, s);  // two splits or more each
-  lc.cfg.gridDim.y = kRows / 32;
+  lc.cfg.gridDim.y = kRows / kJoinRows;
   return check_cuda(cudaLaunchKernelEx(&lc.cfg, attention_kv4_prompt_join<G>, a, min_rows, sm_count(), parts_of<G>(n.parts, workspace)),
                     "attention_kv4 prompt join launch");
 }
