@@ -150,6 +150,13 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _stream_of(dev: int) -> int:
+    """The current CUDA stream of device `dev` as a raw handle."""
+    if _current_raw_stream is not None:
+        return _current_raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _ptr(t: torch.Tensor | None):
     # a plain int: ctypes turns it into the c_void_p argument itself
     return None if t is None else t.data_ptr()
@@ -575,27 +582,34 @@ def gemm_w4a16_noalloc(x: torch.Tensor, qweight: torch.Tensor, scale: torch.Tens
 _HALF = (torch.float16, torch.bfloat16)
 
 
-def _one_device(**tensors) -> torch.device:
-    """The CUDA device that all given tensors (None: absent) lie on."""
+def _one_device(names: str, *tensors) -> int:
+    """Index of the CUDA device that all given tensors (None: absent) lie on; names: theirs, for the error."""
     dev = None
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError(f"{names.split()[i]} must be a CUDA tensor (no CPU path)")
+            if dev is not None:
+                raise ValueError(f"{names.split()[i]} is on {t.device}, other arguments on cuda:{dev}")
+            dev = d
     return dev
 
 
 _SAME_DEVICE = contextlib.nullcontext()
 
 
-def _on(dev: torch.device):
-    """A context in which `dev` is the current device (and _stream() its stream)."""
-    return _SAME_DEVICE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _call(fn, args, dev: int, where: str) -> None:
+    """Issue a C call on the current stream of device `dev`."""
+    if dev == torch.cuda.current_device():
+        st = fn(*args, _stream_of(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream_of(dev))
+    if st != QG_OK:
+        raise QGError(st, where)
 
 
 def _half_code(t: torch.Tensor, name: str) -> int:
@@ -605,13 +619,13 @@ def _half_code(t: torch.Tensor, name: str) -> int:
 
 
 def _shape2(t: torch.Tensor, name: str, M: int, K: int) -> None:
-    if tuple(t.shape) != (M, K):
+    if t.shape != (M, K):
         raise ValueError(f"{name} must be [{M}, {K}], got {tuple(t.shape)}")
 
 
 def _rmsnorm_args(x, weight, residual, eps, out, scale_out, residual_out):
     """((xq, x_scale, h or None), device, the C arguments but the stream) of qg_rmsnorm_quantize_int8."""
-    dev = _one_device(x=x, weight=weight, residual=residual, out=out, scale_out=scale_out, residual_out=residual_out)
+    dev = _one_device("x weight residual out scale_out residual_out", x, weight, residual, out, scale_out, residual_out)
     code = _half_code(x, "x")
     ldx = _rowmajor(x, "x", x.dtype)
     M, K = x.shape
@@ -643,15 +657,14 @@ def rmsnorm_quantize_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch
     (qg_rmsnorm_quantize_int8) -> (xq, x_scale, h); h is None without a residual.
     residual_out may be residual or x itself."""
     r, dev, a = _rmsnorm_args(x, weight, residual, eps, out, scale_out, residual_out)
-    with _on(dev):
-        _check(raw.qg_rmsnorm_quantize_int8(*a, _stream()), "qg_rmsnorm_quantize_int8")
+    _call(raw.qg_rmsnorm_quantize_int8, a, dev, "qg_rmsnorm_quantize_int8")
     return r
 
 
 def dequantize_rowwise_int8(xq: torch.Tensor, x_scale: torch.Tensor, out_dtype: torch.dtype = torch.float16,
                             out: torch.Tensor | None = None) -> torch.Tensor:
     """The values xq * x_scale of int8 rows (qg_dequantize_rowwise_int8)."""
-    dev = _one_device(xq=xq, x_scale=x_scale, out=out)
+    dev = _one_device("xq x_scale out", xq, x_scale, out)
     if out_dtype not in (torch.float32, *_HALF):
         raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {out_dtype}")
     ldq = _rowmajor(xq, "xq", torch.int8)
@@ -661,9 +674,8 @@ def dequantize_rowwise_int8(xq: torch.Tensor, x_scale: torch.Tensor, out_dtype: 
         out = torch.empty((M, (K + 7) // 8 * 8), dtype=out_dtype, device=dev)[:, :K]
     ldy = _rowmajor(out, "out", out_dtype)
     _shape2(out, "out", M, K)
-    with _on(dev):
-        _check(raw.qg_dequantize_rowwise_int8(_ptr(xq), ldq, _ptr(x_scale), _ptr(out), _DTYPE_CODE[out_dtype], ldy,
-                                              M, K, _stream()), "qg_dequantize_rowwise_int8")
+    _call(raw.qg_dequantize_rowwise_int8, (_ptr(xq), ldq, _ptr(x_scale), _ptr(out), _DTYPE_CODE[out_dtype], ldy, M, K), dev,
+          "qg_dequantize_rowwise_int8")
     return out
 
 
@@ -698,6 +710,9 @@ class KV4Cache(NamedTuple):
         return 64 * self.k_codes.shape[4]
 
 
+_CACHE_NAMES = " ".join(KV4Cache._fields)
+
+
 def kv4_cache(num_pages: int, num_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> KV4Cache:
     """A zero-filled KV4Cache."""
     if head_dim not in (64, 128) or page_size <= 0 or page_size % 16:
@@ -726,7 +741,7 @@ def _heads3(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
     """Token and head strides of a [T, H, D] tensor with unit inner stride."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
     st = t.stride()
     if st[2] != 1:
@@ -741,7 +756,7 @@ def _slots(slots: torch.Tensor, T: int) -> torch.Tensor:
 
 def _quantize_kv4_args(k, v, cache, slots):
     """(tensors to keep, device, the C arguments but the stream) of qg_quantize_kv4."""
-    dev = _one_device(k=k, v=v, slots=slots, **cache._asdict())
+    dev = _one_device("k v slots " + _CACHE_NAMES, k, v, slots, *cache)
     c = _cache_arg(cache)
     code = _half_code(k, "k")
     T = k.shape[0]
@@ -756,8 +771,7 @@ def quantize_kv4(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: torch
     `slots` int64 [T] (page * page_size + offset; negative: skipped), in place
     (qg_quantize_kv4)."""
     _, dev, a = _quantize_kv4_args(k, v, cache, slots)
-    with _on(dev):
-        _check(raw.qg_quantize_kv4(*a, _stream()), "qg_quantize_kv4")
+    _call(raw.qg_quantize_kv4, a, dev, "qg_quantize_kv4")
     return cache
 
 
@@ -770,20 +784,19 @@ def dequantize_kv4(cache: KV4Cache, slots: torch.Tensor, out_dtype: torch.dtype 
     if out is None:
         out = tuple(torch.empty(shape, dtype=out_dtype, device=cache.k_codes.device) for _ in range(2))
     k, v = out
-    dev = _one_device(slots=slots, k=k, v=v, **cache._asdict())
+    dev = _one_device("slots k v " + _CACHE_NAMES, slots, k, v, *cache)
     c = _cache_arg(cache)
     ks, vs = _heads3(k, "out[0]", out_dtype, shape), _heads3(v, "out[1]", out_dtype, shape)
     _slots(slots, T)
-    with _on(dev):
-        _check(raw.qg_dequantize_kv4(ctypes.byref(c), _ptr(slots), _ptr(k), *ks, _ptr(v), *vs, _DTYPE_CODE[out_dtype],
-                                     T, _stream()), "qg_dequantize_kv4")
+    _call(raw.qg_dequantize_kv4, (ctypes.byref(c), _ptr(slots), _ptr(k), *ks, _ptr(v), *vs, _DTYPE_CODE[out_dtype], T), dev,
+          "qg_dequantize_kv4")
     return k, v
 
 
 def _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal, window, out, lse):
     """(out, workspace, tensors to keep, device, the C arguments but the stream) of qg_attention_kv4."""
-    dev = _one_device(q=q, block_table=block_table, seq_lens=seq_lens, q_starts=q_starts, out=out, lse=lse,
-                      **cache._asdict())
+    dev = _one_device("q block_table seq_lens q_starts out lse " + _CACHE_NAMES, q, block_table, seq_lens, q_starts, out,
+                      lse, *cache)
     c = _cache_arg(cache)
     code = _half_code(q, "q")
     if q.dim() != 3:
@@ -804,7 +817,7 @@ def _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal
         if lse.dtype is not torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous float32 [{T}, {Hq}]")
     scale = cache.head_dim ** -0.5 if scale is None else float(scale)
-    with _on(dev):
+    with _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev):
         need = int(raw.qg_attention_kv4_workspace_size(B, T, Hq, cache.num_heads, cache.head_dim,
                                                        int(q_starts is not None)))
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
@@ -822,8 +835,7 @@ def attention_kv4(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, s
     gives each sequence's rows of q (None: T / B each).  scale defaults to
     head_dim ** -0.5.  lse float32 [T, heads_q] receives the log-sum-exp."""
     out, _, dev, a = _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal, window, out, lse)
-    with _on(dev):
-        _check(raw.qg_attention_kv4(*a, _stream()), "qg_attention_kv4")
+    _call(raw.qg_attention_kv4, a, dev, "qg_attention_kv4")
     return out
 
 
@@ -844,13 +856,13 @@ class Plan:
 
     __slots__ = ("_h", "_keep", "out", "_dev")
 
-    def __init__(self, handle: int, keep: tuple, out, dev: torch.device | None = None):
+    def __init__(self, handle: int, keep: tuple, out, dev: int | None = None):
         self._h, self._keep, self.out, self._dev = handle, keep, out, dev
 
     def launch(self, stream=None) -> None:
         """Issue the call on `stream` (a torch.cuda.Stream or a raw handle;
         default: the current stream)."""
-        if self._dev is not None and self._dev.index != torch.cuda.current_device():
+        if self._dev is not None and self._dev != torch.cuda.current_device():
             with torch.cuda.device(self._dev):
                 return self.launch(stream)
         s = _stream() if stream is None else getattr(stream, "cuda_stream", stream)
@@ -870,7 +882,7 @@ class Plan:
         self.close()
 
 
-def _new_plan(fn, args, keep, out, where: str, dev: torch.device | None = None) -> Plan:
+def _new_plan(fn, args, keep, out, where: str, dev: int | None = None) -> Plan:
     h = ctypes.c_void_p()
     _check(fn(ctypes.byref(h), *args), where)
     return Plan(h.value, keep, out, dev)
