@@ -12,7 +12,9 @@
 // IEEE operations, whatever the order of the sum of squares.
 //
 // Memory-bound: 7 bytes per element with a residual (x, residual in; h and
-// the code out), 3 without.
+// the code out), 3 without; the reader 3 (fp16, bf16) or 5 (fp32).
+// 8192 x 4096 with a residual: 37.8 us (6.2 TB/s), reader 17.0 us (5.9 TB/s);
+// 1 x 4096: 2.3 and 1.1 us in a row of launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -228,14 +230,25 @@ cudaError_t launch_norm(const void* x, int64_t ldx, const void* residual, int64_
     return cudaLaunchKernelEx(&lc.cfg, kernel, static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr,
                               static_cast<const T*>(weight), eps, xq, ldq, xs, static_cast<T*>(res_out), ldo, M, K);
   };
-  // the row stays in registers up to 8 x 4 x 512 elements
-  if (K <= 1024) return go(rmsnorm_quantize_kernel<T, 32, 8, 4>, 32, 8);
-  if (K <= 4096) return go(rmsnorm_quantize_kernel<T, 128, 2, 4>, 128, 2);
+  // The row stays in registers up to 8 x 4 x 512 elements.  Few threads with much in flight each carry many rows, more
+  // threads shorten the few (us with a residual, chosen / the other):
+  //   K <= 1024        1 x 1024: 1.7 / 2.4; 32768 x 1024: 41.9 / 37.2; 65536 x 512, 32 threads a row: 41.5 / 49.8 (64)
+  //   K <= 4096        333 x 4096: 3.8 / 4.9 (256 threads); 8192 x 4096: 37.8 / 53.6 (512), 45.5 (two rows of 128 a block)
+  //   K <= 16384       1 x 10007: 3.7 / 4.1 (256 threads); 333 x 10007: 6.1 / 8.1 (512)
+  const int sms = sm_count();
+  if (K <= 1024) {
+    if (M <= 4 * sms) return go(rmsnorm_quantize_kernel<T, 128, 1, 1>, 128, 1);
+    if (K <= 512) return go(rmsnorm_quantize_kernel<T, 32, 4, 4>, 32, 4);
+    return go(rmsnorm_quantize_kernel<T, 64, 2, 2>, 64, 2);
+  }
+  if (K <= 2048) return go(rmsnorm_quantize_kernel<T, 128, 1, 2>, 128, 1);
+  if (K <= 4096 && M > 4 * sms) return go(rmsnorm_quantize_kernel<T, 256, 1, 2>, 256, 1);
+  if (K <= 8192) return go(rmsnorm_quantize_kernel<T, 512, 1, 2>, 512, 1);
+  if (K <= 16384 && M > sms) return go(rmsnorm_quantize_kernel<T, 256, 1, 8>, 256, 1);
   if (K <= 16384) return go(rmsnorm_quantize_kernel<T, 512, 1, 4>, 512, 1);
   return go(rmsnorm_quantize_kernel<T, 512, 1, 0>, 512, 1);
 }
 
-// 8 codes per thread and step, VEC steps in flight.
 template <typename T>
 __device__ __forceinline__ void store8(T* y, const float (&v)[8]);
 template <>
@@ -255,50 +268,86 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* y, const fl
                  pair_bits<__nv_bfloat16>(v[4], v[5]), pair_bits<__nv_bfloat16>(v[6], v[7]));
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(256) dequantize_rowwise_kernel(const int8_t* __restrict__ xq, int64_t ldq,
+template <typename T>
+__device__ __forceinline__ void read8(uint2 c, float s, T* y) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[k] = __fmul_rn((float)(int8_t)(c.x >> (8 * k)), s);
+    v[4 + k] = __fmul_rn((float)(int8_t)(c.y >> (8 * k)), s);
+  }
+  store8<T>(y, v);
+}
+
+// Block of 128 threads, threadIdx.x along a row, 8 codes a thread and load, VEC loads in flight: along the row, or
+// (BY_ROWS, short rows) of VEC rows.
+template <typename T, int VEC, bool BY_ROWS>
+__global__ void __launch_bounds__(128) dequantize_rowwise_kernel(const int8_t* __restrict__ xq, int64_t ldq,
                                                                  const float* __restrict__ xs, T* __restrict__ y,
                                                                  int64_t ldy, int M, int K) {
   pdl_trigger();
   pdl_wait();
-  const int nvec = K / 8, t = threadIdx.x, first = blockIdx.y * (256 * VEC) + t;
-  for (int m = blockIdx.x; m < M; m += gridDim.x) {
-    const int8_t* q = xq + (int64_t)m * ldq;
-    T* out = y + (int64_t)m * ldy;
-    const float s = __ldg(xs + m);
+  const int nvec = K / 8, t = threadIdx.x, kt = nvec * 8 + t;
+  if constexpr (BY_ROWS) {
+    const int across = blockDim.x, down = blockDim.y;  // down: rows at a time
+    const int64_t row0 = (int64_t)blockIdx.x * (VEC * down) + threadIdx.y;
+    float s[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[j] = row0 + j * down < M ? __ldg(xs + row0 + j * down) : 0.0f;
 #pragma unroll 1
-    for (int64_t base = first; base < nvec; base += (int64_t)gridDim.y * (256 * VEC)) {
+    for (int i = t; i < nvec; i += across) {
       uint2 c[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        if (base + 256 * j < nvec) c[j] = __ldg(reinterpret_cast<const uint2*>(q) + base + 256 * j);
+        if (row0 + j * down < M) c[j] = __ldg(reinterpret_cast<const uint2*>(xq + (row0 + j * down) * ldq) + i);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if (base + 256 * j >= nvec) break;
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = __fmul_rn((float)(int8_t)(c[j].x >> (8 * k)), s);
-          v[4 + k] = __fmul_rn((float)(int8_t)(c[j].y >> (8 * k)), s);
-        }
-        store8<T>(out + 8 * (base + 256 * j), v);
-      }
+      for (int j = 0; j < VEC; ++j)
+        if (row0 + j * down < M) read8<T>(c[j], s[j], y + (row0 + j * down) * ldy + 8 * i);
     }
-    const int kt = nvec * 8 + t;
-    if (blockIdx.y == 0 && kt < K) out[kt] = (T)__fmul_rn((float)q[kt], s);
+    if (kt < K)
+      for (int j = 0; j < VEC; ++j)
+        if (row0 + j * down < M) y[(row0 + j * down) * ldy + kt] = (T)__fmul_rn((float)xq[(row0 + j * down) * ldq + kt], s[j]);
+  } else {
+    const int first = blockIdx.y * (128 * VEC) + t;
+    for (int m = blockIdx.x; m < M; m += gridDim.x) {
+      const int8_t* q = xq + (int64_t)m * ldq;
+      T* out = y + (int64_t)m * ldy;
+      const float s = __ldg(xs + m);
+#pragma unroll 1
+      for (int64_t base = first; base < nvec; base += (int64_t)gridDim.y * (128 * VEC)) {
+        uint2 c[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (base + 128 * j < nvec) c[j] = __ldg(reinterpret_cast<const uint2*>(q) + base + 128 * j);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (base + 128 * j < nvec) read8<T>(c[j], s, out + 8 * (base + 128 * j));
+      }
+      if (blockIdx.y == 0 && kt < K) out[kt] = (T)__fmul_rn((float)q[kt], s);
+    }
   }
 }
 
 template <typename T>
 cudaError_t launch_dequant(const int8_t* xq, int64_t ldq, const float* xs, void* y, int64_t ldy, int M, int K,
                            cudaStream_t s) {
-  auto go = [&](auto kernel, int vec) {
-    const int64_t gy = std::max(1, (K / 8 + 256 * vec - 1) / (256 * vec));
-    LaunchCfg lc((unsigned)std::min<int64_t>(M, ((int64_t)1 << 31) - 1), 256, 0, s);
-    lc.cfg.gridDim.y = (unsigned)std::min<int64_t>(gy, 65535);
+  const auto go = [&](auto kernel, LaunchCfg& lc) {
     return cudaLaunchKernelEx(&lc.cfg, kernel, xq, ldq, xs, static_cast<T*>(y), ldy, M, K);
   };
-  return K <= 2048 ? go(dequantize_rowwise_kernel<T, 1>, 1) : go(dequantize_rowwise_kernel<T, 2>, 2);
+  const int nvec = K / 8;
+  // few elements: one load a thread (1 x 4096: 1.1 us, four loads 1.5; 8192 x 4096: 34 and 17)
+  const int vec = (int64_t)M * nvec <= (int64_t)sm_count() * 512 ? 1 : 4;
+  if (K <= 2048) {  // a block of 128 threads a row would idle or load once (us by rows and not: 32768 x 1024 17, 34)
+    int across = 8;
+    while (across < std::min(nvec, 128)) across *= 2;
+    const int down = 128 / across;
+    LaunchCfg lc((unsigned)(((int64_t)M + vec * down - 1) / (vec * down)), (unsigned)across, 0, s);
+    lc.cfg.blockDim.y = (unsigned)down;
+    return vec == 1 ? go(dequantize_rowwise_kernel<T, 1, true>, lc) : go(dequantize_rowwise_kernel<T, 4, true>, lc);
+  }
+  LaunchCfg lc((unsigned)M, 128, 0, s);
+  lc.cfg.gridDim.y = (unsigned)std::min(std::max(1, (nvec + 128 * vec - 1) / (128 * vec)), 65535);
+  return vec == 1 ? go(dequantize_rowwise_kernel<T, 1, false>, lc) : go(dequantize_rowwise_kernel<T, 4, false>, lc);
 }
 
 }  // namespace
