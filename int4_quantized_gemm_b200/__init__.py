@@ -710,7 +710,8 @@ class KV4Cache(NamedTuple):
         return 64 * self.k_codes.shape[4]
 
 
-_CACHE_NAMES = " ".join(KV4Cache._fields)
+_WRITE_NAMES, _READ_NAMES, _ATTENTION_NAMES = (
+    a + " " + " ".join(KV4Cache._fields) for a in ("k v slots", "slots k v", "q block_table seq_lens q_starts out lse"))
 
 
 def kv4_cache(num_pages: int, num_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> KV4Cache:
@@ -723,18 +724,20 @@ def kv4_cache(num_pages: int, num_heads: int, head_dim: int, page_size: int = 64
 
 
 def _cache_arg(cache: KV4Cache) -> _CKV4Cache:
-    kc = cache.k_codes
-    if kc.dim() != 5 or kc.shape[3] != 8:
-        raise ValueError(f"codes must be [num_pages, num_heads, page_size, 8, head_dim / 64], got {tuple(kc.shape)}")
-    n, h, p, _, g = kc.shape
-    for t, name, dtype, shape in ((kc, "k_codes", torch.int32, (n, h, p, 8, g)),
-                                  (cache.v_codes, "v_codes", torch.int32, (n, h, p, 8, g)),
-                                  (cache.k_params, "k_params", torch.float16, (n, h, p, g, 2)),
-                                  (cache.v_params, "v_params", torch.float16, (n, h, p, g, 2))):
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
-    return _CKV4Cache(kc.data_ptr(), cache.k_params.data_ptr(), cache.v_codes.data_ptr(), cache.v_params.data_ptr(),
-                      n, h, p, 64 * g)
+    kc, kp, vc, vp = cache
+    codes = kc.shape
+    if len(codes) != 5 or codes[3] != 8:
+        raise ValueError(f"codes must be [num_pages, num_heads, page_size, 8, head_dim / 64], got {tuple(codes)}")
+    n, h, p, _, g = codes
+    params = (n, h, p, g, 2)
+    if not (kc.dtype is vc.dtype is torch.int32 and kp.dtype is vp.dtype is torch.float16 and vc.shape == codes
+            and kp.shape == params and vp.shape == params and kc.is_contiguous() and vc.is_contiguous()
+            and kp.is_contiguous() and vp.is_contiguous()):
+        for t, name, dtype, shape in ((kc, "k_codes", torch.int32, tuple(codes)), (vc, "v_codes", torch.int32, tuple(codes)),
+                                      (kp, "k_params", torch.float16, params), (vp, "v_params", torch.float16, params)):
+            if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
+    return _CKV4Cache(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), n, h, p, 64 * g)
 
 
 def _heads3(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
@@ -756,11 +759,11 @@ def _slots(slots: torch.Tensor, T: int) -> torch.Tensor:
 
 def _quantize_kv4_args(k, v, cache, slots):
     """(tensors to keep, device, the C arguments but the stream) of qg_quantize_kv4."""
-    dev = _one_device("k v slots " + _CACHE_NAMES, k, v, slots, *cache)
+    dev = _one_device(_WRITE_NAMES, k, v, slots, *cache)
     c = _cache_arg(cache)
     code = _half_code(k, "k")
     T = k.shape[0]
-    shape = (T, cache.num_heads, cache.head_dim)
+    shape = (T, c.num_heads, c.head_dim)
     ks, vs = _heads3(k, "k", k.dtype, shape), _heads3(v, "v", k.dtype, shape)
     _slots(slots, T)
     return (k, v, cache, slots, c), dev, (_ptr(k), *ks, _ptr(v), *vs, code, _ptr(slots), ctypes.byref(c), T)
@@ -778,14 +781,15 @@ def quantize_kv4(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: torch
 def dequantize_kv4(cache: KV4Cache, slots: torch.Tensor, out_dtype: torch.dtype = torch.float16, out=None):
     """Keys and values [T, num_heads, head_dim] of the tokens at `slots`, zeros at
     a negative slot (qg_dequantize_kv4).  out: (k, v) to write into."""
-    T, shape = slots.numel(), (slots.numel(), cache.num_heads, cache.head_dim)
     if out_dtype not in (torch.float32, *_HALF):
         raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {out_dtype}")
+    c = _cache_arg(cache)
+    T = slots.numel()
+    shape = (T, c.num_heads, c.head_dim)
     if out is None:
         out = tuple(torch.empty(shape, dtype=out_dtype, device=cache.k_codes.device) for _ in range(2))
     k, v = out
-    dev = _one_device("slots k v " + _CACHE_NAMES, slots, k, v, *cache)
-    c = _cache_arg(cache)
+    dev = _one_device(_READ_NAMES, slots, k, v, *cache)
     ks, vs = _heads3(k, "out[0]", out_dtype, shape), _heads3(v, "out[1]", out_dtype, shape)
     _slots(slots, T)
     _call(raw.qg_dequantize_kv4, (ctypes.byref(c), _ptr(slots), _ptr(k), *ks, _ptr(v), *vs, _DTYPE_CODE[out_dtype], T), dev,
@@ -795,7 +799,7 @@ def dequantize_kv4(cache: KV4Cache, slots: torch.Tensor, out_dtype: torch.dtype 
 
 def _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal, window, out, lse):
     """(out, workspace, tensors to keep, device, the C arguments but the stream) of qg_attention_kv4."""
-    dev = _one_device("q block_table seq_lens q_starts out lse " + _CACHE_NAMES, q, block_table, seq_lens, q_starts, out,
+    dev = _one_device(_ATTENTION_NAMES, q, block_table, seq_lens, q_starts, out,
                       lse, *cache)
     c = _cache_arg(cache)
     code = _half_code(q, "q")
@@ -803,7 +807,8 @@ def _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal
         raise ValueError(f"q must be [T, heads_q, head_dim], got {tuple(q.shape)}")
     T, Hq, _ = q.shape
     B = seq_lens.numel()
-    shape = (T, Hq, cache.head_dim)
+    heads, dim = c.num_heads, c.head_dim
+    shape = (T, Hq, dim)
     qs = _heads3(q, "q", q.dtype, shape)
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=dev)
@@ -816,10 +821,9 @@ def _attention_kv4_args(q, cache, block_table, seq_lens, q_starts, scale, causal
     if lse is not None:
         if lse.dtype is not torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous float32 [{T}, {Hq}]")
-    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+    scale = dim ** -0.5 if scale is None else float(scale)
     with _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev):
-        need = int(raw.qg_attention_kv4_workspace_size(B, T, Hq, cache.num_heads, cache.head_dim,
-                                                       int(q_starts is not None)))
+        need = int(raw.qg_attention_kv4_workspace_size(B, T, Hq, heads, dim, int(q_starts is not None)))
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     return out, (q, cache, block_table, seq_lens, q_starts, out, lse, ws, c), dev, (
         _ptr(q), *qs, ctypes.byref(c), _ptr(block_table), ld, _ptr(seq_lens), _ptr(q_starts), scale, int(causal),
