@@ -3,22 +3,40 @@
 // decode kernel takes (prompts, chunks of prompts, long drafts).
 //
 // Compute-bound: 4 dim operations and one exponential per (row, key).  One CTA
-// takes 256 rows (two tiles of 128) of a (sequence, KV head) and walks over the
-// keys 64 at a time:
+// takes 256 rows (two tiles of 128, so that both share a step's dequantized keys
+// and values) of a (sequence, KV head) and walks over the keys 64 at a time:
+//   2 MMA warps      one per row tile; tcgen05: S = Q K^T (M 128, N 64, K dim)
+//                    and O += P V (P from tensor memory, N dim), accumulators in
+//                    tensor memory: 2 x 2 x 64 columns S, 2 x dim columns O
 //   2 loader warps   packed codes and params of 64 tokens a stage, bulk copies,
 //                    keys and values in rings of their own
-//   2 x 4 warps      codes -> fp16 (c s + o, one rounding) into the swizzled
-//                    K-major operands K [key][channel] and V^T [channel][key];
-//                    both row tiles share them
-//   MMA warp         tcgen05: S = Q K^T (M 128, N 64, K dim) and O += P V
-//                    (P from tensor memory, N dim), accumulators in tensor memory
 //   2 x 4 warps      softmax of a row tile, a thread per row: maximum, p =
 //                    2^(x - m), P in fp16 over S's columns
+//   2 x 4 warps      codes -> fp16 (c s + o, one rounding) into the swizzled
+//                    K-major operands K [key][channel] and V^T [channel][key]
 // Scores of a row tile alternate between two places in tensor memory and run
-// two steps ahead, so its softmax never waits for the products of its own
-// probabilities.  The maximum that scores are taken against moves only when a row passes it by 8
-// binary digits, so the accumulator is rarely rescaled; p carries a factor 2^7
-// that keeps small ones out of fp16's subnormals (p 2^7 < 2^15).
+// two steps ahead, so its softmax does not wait for the products of its own
+// probabilities.  The maximum that scores are taken against moves only when a
+// row passes it by 8 binary digits, so the accumulator is rarely rescaled; p
+// carries a factor 2^7 that keeps small ones out of fp16's subnormals (p 2^7 <
+// 2^15).
+//
+// Roundings to fewer than 32 bits, all to fp16 because the tensor cores take two
+// 16-bit operands: queries (exact for fp16; bf16 has fewer digits and is scaled
+// into fp16's range), a key's and a value's c s + o, and p.  Each is half a step
+// of 2^-11; scores, maxima, sums and outputs are binary32.  (At 2 x 4096 tokens
+// of fp16 they make 0.00037 of relative error beside the output's own rounding
+// of 0.00021: keys 0.00027, values 0.00020, p 0.00015.  Splitting keys into two
+// operands would take the first away for 1.4 times the tensor cores' time.)
+//
+// 2 x 4096 tokens, 32 heads of 128, causal: 340 us, 0.81 PFLOP/s.  A step of 64
+// keys by 256 rows takes 2250 cycles.  The tensor pipe is busy for 1590 of them
+// (a product of N 64 reads both operands from shared memory and takes 65 cycles
+// instead of 32); exponentials need 1024 of the MUFU.  The two tiles share both
+// units in phase, which leaves the rest.  Tried and slower: scores of 128 keys
+// at once (one place for S, 419 us), tiles taking turns at the tensor cores
+// (390), the maximum beside the exponentials of a stale one (361), a part of the
+// exponentials as polynomials.
 //
 // Channels of K and Q lie in the order 0 4 1 5 2 6 3 7 of each 8 (the order in
 // which masks take nibbles from a word); row 8 i + j of a V^T group is channel
@@ -26,7 +44,8 @@
 // output's columns back.
 //
 // With few (rows, head)s the keys are split over CTAs whose parts a second
-// kernel joins in order.
+// kernel joins in order (16 sequences of 4096 tokens, two with 64 new tokens: 65
+// us, 98 without).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -378,120 +397,120 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // each group of four warps changes its registers at the head of its own branch
   if (warp < kSoftmaxWarp) {
-   regs_down<kOtherRegs>();
-   if (warp >= kLoadWarp) {
-    // ---- packed codes and params: one warp for the keys' ring, one for the values' ---------
-    const int ring = warp - kLoadWarp;
-    const uint32_t base = sm + (ring ? L::values : L::keys), stage_bytes = ring ? L::kValueStage : L::kKeyStage;
-    const int P = a.cache.page_size;
-    const int piece = min(kKeys, P & -P), pieces = kKeys / piece;
-    const int arr = lane / pieces, pc = lane % pieces;  // 0 codes, 1 params, 2 (keys' ring) the values' params
-    const int arrays = ring ? 2 : 3;
-    const uint32_t bytes = arr == 0 ? piece * (D / 2) : piece * (G * 4);
-    const uint32_t dst_off = (arr == 0 ? 0 : L::kCodes + (arr - 1) * L::kParams) + pc * bytes;
-    const uint32_t code_lanes = (1u << pieces) - 1;
-    const uint32_t* src = arr == 0 ? (ring ? a.cache.codes[1] : a.cache.codes[0])
-                                   : (ring || arr == 2 ? a.cache.params[1] : a.cache.params[0]);
-    int issued = 0;
+    regs_down<kOtherRegs>();
+    if (warp >= kLoadWarp) {
+      // ---- packed codes and params: one warp for the keys' ring, one for the values' ---------
+      const int ring = warp - kLoadWarp;
+      const uint32_t base = sm + (ring ? L::values : L::keys), stage_bytes = ring ? L::kValueStage : L::kKeyStage;
+      const int P = a.cache.page_size;
+      const int piece = min(kKeys, P & -P), pieces = kKeys / piece;
+      const int arr = lane / pieces, pc = lane % pieces;  // 0 codes, 1 params, 2 (keys' ring) the values' params
+      const int arrays = ring ? 2 : 3;
+      const uint32_t bytes = arr == 0 ? piece * (D / 2) : piece * (G * 4);
+      const uint32_t dst_off = (arr == 0 ? 0 : L::kCodes + (arr - 1) * L::kParams) + pc * bytes;
+      const uint32_t code_lanes = (1u << pieces) - 1;
+      const uint32_t* src = arr == 0 ? (ring ? a.cache.codes[1] : a.cache.codes[0])
+                                     : (ring || arr == 2 ? a.cache.params[1] : a.cache.params[0]);
+      int issued = 0;
 #pragma unroll 1
-    for (int i = 0; i < total; ++i) {
-      int page = -1, in_page = 0;
-      const int t = first_step * kKeys + i * kKeys + pc * piece;
-      if (arr < arrays && t < job.len) {
-        const int pi = (int)kv4_page(a.cache, (uint32_t)t >> 4);
-        in_page = t - pi * P;
-        page = __ldg(a.table + (int64_t)job.b * a.table_ld + pi);
-        if (page < 0 || page >= a.cache.pages) {
-          report(kDevBadArg, kSitePage);
-          page = -1;
+      for (int i = 0; i < total; ++i) {
+        int page = -1, in_page = 0;
+        const int t = first_step * kKeys + i * kKeys + pc * piece;
+        if (arr < arrays && t < job.len) {
+          const int pi = (int)kv4_page(a.cache, (uint32_t)t >> 4);
+          in_page = t - pi * P;
+          page = __ldg(a.table + (int64_t)job.b * a.table_ld + pi);
+          if (page < 0 || page >= a.cache.pages) {
+            report(kDevBadArg, kSitePage);
+            page = -1;
+          }
+        }
+        const int st = i % kRaw;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&raw_empty[ring][st]), (i / kRaw & 1) ^ 1, &g_status_prompt, kSiteRawEmpty))) break;
+        const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+        const uint32_t bar = smem_u32(&raw_full[ring][st]);
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar, __popc(have & code_lanes) * (uint32_t)(piece * (D / 2)) +
+                                         __popc(have & ~code_lanes) * (uint32_t)(piece * (G * 4)));
+        __syncwarp();
+        if (page >= 0) {
+          const int64_t r = kv4_row(a.cache, page, job.h) + in_page;
+          bulk_load(base + st * stage_bytes + dst_off, src + r * (arr == 0 ? D / 8 : G), bytes, bar);
+        }
+        issued = i + 1;
+      }
+      // no copy in flight outlives the CTA
+      for (int i = max(0, issued - kRaw); i < issued; ++i)
+        mbar_wait(smem_u32(&raw_full[ring][i % kRaw]), i / kRaw & 1, &g_status_prompt, kSiteDrain);
+    } else {
+      // ---- tensor cores, row tile `warp` ---------------------------------------------------------
+      // The whole warp runs this with warp-uniform operands and one elected lane issues: from a branch of one lane the
+      // operands go through vector registers and an MMA costs 175 cycles instead of 65.
+      constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys), kIdescO = idesc_f16_f32(128, D);
+      // descriptors of the operands' first blocks; a step along K or a block further only adds to the address field
+      const uint64_t dq = sdesc_sw128(sm + L::q), dk = sdesc_sw128(sm + L::k), dv = sdesc_sw128(sm + L::v);
+      const uint32_t um_s = __shfl_sync(0xffffffffu, tm_s, 0), um_o = __shfl_sync(0xffffffffu, tm_o, 0);
+      const int t = __shfl_sync(0xffffffffu, warp, 0), mine = steps[t];
+      const auto scores = [&](int i) {
+        const uint64_t q = dq + (uint32_t)t * (L::kOperand >> 4), k = dk + (uint32_t)(i % kBuf) * (L::kStep >> 4);
+        const uint32_t d = um_s + (i & 1) * 64 + t * 128;
+        if (elect_one()) {
+          mma_first(d, q, k, kIdescS);
+#pragma unroll
+          for (int n = 1; n < 4 * G; ++n)
+            mma_next(d, q + (uint32_t)((n / 4 * L::kBlock + n % 4 * 32) >> 4),
+                     k + (uint32_t)((n / 4 * (kKeys * 128) + n % 4 * 32) >> 4), kIdescS);
+          mma_commit(smem_u32(&s_full[t][i & 1]));
+          mma_commit(smem_u32(&k_empty[i % kBuf]));
+        }
+        __syncwarp();
+      };
+      const auto outputs = [&](int i) {
+        const uint64_t v = dv + (uint32_t)(i % kBuf) * (L::kStep >> 4);
+        const uint32_t d = um_o + t * D, p = um_s + (i & 1) * 64 + t * 128;
+        if (elect_one()) {
+          mma_f16_ts(d, p, v, kIdescO, i > 0);
+#pragma unroll
+          for (int n = 1; n < 4; ++n) mma_next_ts(d, p + n * 8, v + (uint32_t)(n * 32 >> 4), kIdescO);
+          mma_commit(smem_u32(&o_done[t][i & 1]));
+          mma_commit(smem_u32(&v_empty[i % kBuf]));
+        }
+        __syncwarp();
+      };
+      const auto wait = [&](uint64_t& bar, int parity, uint32_t site) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &g_status_prompt, site));
+        tc_fence_after();
+        return ok;
+      };
+      // Scores run two steps ahead of the outputs, into the columns whose P the product before them has read (the
+      // tensor cores work in order): a tile's next scores are there when its softmax comes to them.
+      bool ok = mine == 0 || wait(q_full[t], 0, kSiteQ);
+#pragma unroll 1
+      for (int i = -2; i < mine && ok; ++i) {
+        const int next = i + 2;
+        if (i >= 0) {
+          ok = wait(v_full[i % kBuf], i / kBuf & 1, kSiteVFull) && wait(p_full[t][i & 1], i >> 1 & 1, kSiteP);
+          if (ok) outputs(i);
+        }
+        if (ok && next < mine) {
+          ok = wait(k_full[next % kBuf], next / kBuf & 1, kSiteKFull);
+          if (ok) scores(next);
         }
       }
-      const int st = i % kRaw;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&raw_empty[ring][st]), (i / kRaw & 1) ^ 1, &g_status_prompt, kSiteRawEmpty))) break;
-      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-      const uint32_t bar = smem_u32(&raw_full[ring][st]);
-      if (lane == 0)
-        mbar_arrive_expect_tx(bar, __popc(have & code_lanes) * (uint32_t)(piece * (D / 2)) +
-                                       __popc(have & ~code_lanes) * (uint32_t)(piece * (G * 4)));
-      __syncwarp();
-      if (page >= 0) {
-        const int64_t r = kv4_row(a.cache, page, job.h) + in_page;
-        bulk_load(base + st * stage_bytes + dst_off, src + r * (arr == 0 ? D / 8 : G), bytes, bar);
-      }
-      issued = i + 1;
-    }
-    // no copy in flight outlives the CTA
-    for (int i = max(0, issued - kRaw); i < issued; ++i)
-      mbar_wait(smem_u32(&raw_full[ring][i % kRaw]), i / kRaw & 1, &g_status_prompt, kSiteDrain);
-   } else {
-    // ---- tensor cores, row tile `warp` ---------------------------------------------------------
-    // The whole warp runs this with warp-uniform operands and one elected lane issues: from a branch of one lane the
-    // operands go through vector registers and an MMA costs 175 cycles instead of 65.
-    constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys), kIdescO = idesc_f16_f32(128, D);
-    // descriptors of the operands' first blocks; a step along K or a block further only adds to the address field
-    const uint64_t dq = sdesc_sw128(sm + L::q), dk = sdesc_sw128(sm + L::k), dv = sdesc_sw128(sm + L::v);
-    const uint32_t um_s = __shfl_sync(0xffffffffu, tm_s, 0), um_o = __shfl_sync(0xffffffffu, tm_o, 0);
-    const int t = __shfl_sync(0xffffffffu, warp, 0), mine = steps[t];
-    const auto scores = [&](int i) {
-      const uint64_t q = dq + (uint32_t)t * (L::kOperand >> 4), k = dk + (uint32_t)(i % kBuf) * (L::kStep >> 4);
-      const uint32_t d = um_s + (i & 1) * 64 + t * 128;
-      if (elect_one()) {
-        mma_first(d, q, k, kIdescS);
-#pragma unroll
-        for (int n = 1; n < 4 * G; ++n)
-          mma_next(d, q + (uint32_t)((n / 4 * L::kBlock + n % 4 * 32) >> 4),
-                   k + (uint32_t)((n / 4 * (kKeys * 128) + n % 4 * 32) >> 4), kIdescS);
-        mma_commit(smem_u32(&s_full[t][i & 1]));
-        mma_commit(smem_u32(&k_empty[i % kBuf]));
-      }
-      __syncwarp();
-    };
-    const auto outputs = [&](int i) {
-      const uint64_t v = dv + (uint32_t)(i % kBuf) * (L::kStep >> 4);
-      const uint32_t d = um_o + t * D, p = um_s + (i & 1) * 64 + t * 128;
-      if (elect_one()) {
-        mma_f16_ts(d, p, v, kIdescO, i > 0);
-#pragma unroll
-        for (int n = 1; n < 4; ++n) mma_next_ts(d, p + n * 8, v + (uint32_t)(n * 32 >> 4), kIdescO);
-        mma_commit(smem_u32(&o_done[t][i & 1]));
-        mma_commit(smem_u32(&v_empty[i % kBuf]));
-      }
-      __syncwarp();
-    };
-    const auto wait = [&](uint64_t& bar, int parity, uint32_t site) {
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, &g_status_prompt, site));
-      tc_fence_after();
-      return ok;
-    };
-    // Scores run two steps ahead of the outputs, into the columns whose P the product before them has read (the
-    // tensor cores work in order): a tile's next scores are there when its softmax comes to them.
-    bool ok = mine == 0 || wait(q_full[t], 0, kSiteQ);
+      // the other tile's further steps want this one's part of their barriers (once the step's own phase has begun)
 #pragma unroll 1
-    for (int i = -2; i < mine && ok; ++i) {
-      const int next = i + 2;
-      if (i >= 0) {
-        ok = wait(v_full[i % kBuf], i / kBuf & 1, kSiteVFull) && wait(p_full[t][i & 1], i >> 1 & 1, kSiteP);
-        if (ok) outputs(i);
+      for (int i = mine; i < total && ok; ++i) {
+        ok = wait(k_full[i % kBuf], i / kBuf & 1, kSiteKFull) && wait(v_full[i % kBuf], i / kBuf & 1, kSiteVFull);
+        if (ok && lane == 0) {
+          mbar_arrive(smem_u32(&k_empty[i % kBuf]));
+          mbar_arrive(smem_u32(&v_empty[i % kBuf]));
+        }
       }
-      if (ok && next < mine) {
-        ok = wait(k_full[next % kBuf], next / kBuf & 1, kSiteKFull);
-        if (ok) scores(next);
-      }
+      if (elect_one()) mma_commit(smem_u32(&drained));
+      __syncwarp();
+      mbar_wait(smem_u32(&drained), 0, &g_status_prompt, kSiteDrain);
+      __syncwarp();
     }
-    // the other tile's further steps want this one's part of their barriers (once the step's own phase has begun)
-#pragma unroll 1
-    for (int i = mine; i < total && ok; ++i) {
-      ok = wait(k_full[i % kBuf], i / kBuf & 1, kSiteKFull) && wait(v_full[i % kBuf], i / kBuf & 1, kSiteVFull);
-      if (ok && lane == 0) {
-        mbar_arrive(smem_u32(&k_empty[i % kBuf]));
-        mbar_arrive(smem_u32(&v_empty[i % kBuf]));
-      }
-    }
-    if (elect_one()) mma_commit(smem_u32(&drained));
-    __syncwarp();
-    mbar_wait(smem_u32(&drained), 0, &g_status_prompt, kSiteDrain);
-    __syncwarp();
-   }
   } else if (warp >= kValueWarp) {
     regs_down<kDequantRegs>();
     // ---- values to fp16: a lane takes one word (8 channels) of 8 tokens and writes 8 tokens of 8 channels ----
@@ -780,7 +799,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; it < kLpr; ++it) {
         const int64_t at = __shfl_sync(0xffffffffu, mine_at, it * kRpi + sub);
         uint4 o;
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "r"(in_row(it * kRpi + sub)));
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                     : "r"(in_row(it * kRpi + sub)));
         if (at >= 0) *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + at + 16 * piece) = o;
       }
     }
