@@ -35,8 +35,8 @@
 // instead of 32); exponentials need 1024 of the MUFU.  The two tiles share both
 // units in phase, which leaves the rest.  Tried and slower: scores of 128 keys
 // at once (one place for S, 419 us), tiles taking turns at the tensor cores
-// (390), the maximum beside the exponentials of a stale one (361), a part of the
-// exponentials as polynomials.
+// (390), two threads a row, 16 warps of softmax (396), the maximum beside the
+// exponentials of a stale one (361), a part of the exponentials as polynomials.
 //
 // Channels of K and Q lie in the order 0 4 1 5 2 6 3 7 of each 8 (the order in
 // which masks take nibbles from a word); row 8 i + j of a V^T group is channel
