@@ -848,9 +848,12 @@ int64_t row_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
 }
 
 // Rows (query tokens x head group) that the decode kernel takes, in tiles of 8; 0: none.  A ragged call gives it
-// the sequences of 8 rows at most (16 where one token has more than 8).
-int decode_tiles(int64_t n, int64_t group, bool ragged) {
-  const int64_t rows = ragged ? group : n * group;
+// the sequences of 8 rows at most, or of 16 where one token has more than 8 or the mean sequence has 9 to 16 (drafts;
+// 64 sequences of 4096..8192 tokens, 32/8 heads of 128, 60 of them with 3 new tokens: 213 us, 488 with the prompt kernel for
+// these; but one of them with 3: 202, 156 with the prompt kernel for it).
+int decode_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
+  int64_t rows = T / B * group;
+  if (ragged) rows = T * group > 8 * B && T * group <= 16 * B ? 16 : group;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : 0;
 }
 
@@ -913,7 +916,7 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t dim, bool ragged) {
   const int64_t group = heads_q / heads;
-  const int nt = decode_tiles(T / B, group, ragged);
+  const int nt = decode_tiles(B, T, group, ragged);
   size_t bytes = nt ? round256(attention_kv4_decode_workspace(dim, nt)) : 0;
   if (!nt || ragged) {
     bytes += (size_t)blocks_of(B, T, group, heads, ragged, nt).parts * kRows * (dim + 2) * sizeof(float);
@@ -924,7 +927,7 @@ size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t he
 // Single tokens and drafts go to the decode kernel, longer ones here; a ragged call launches both and each takes its
 // sequences: first the prompts, then the others on the place that their blocks leave.
 qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s) {
-  const int nt = decode_tiles(a.n_uniform, a.group, a.q_starts != nullptr);
+  const int nt = decode_tiles(a.B, a.T, a.group, a.q_starts != nullptr);
   const bool prompts = !nt || a.q_starts;
   const Blocks n = blocks_of(a.B, a.T, a.group, a.cache.heads, a.q_starts != nullptr, nt);
   const int min_rows = 8 * nt + 1;

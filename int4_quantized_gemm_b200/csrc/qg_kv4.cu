@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Tokens a thread once that still gives every SM eight blocks of threads; else one (latency).  The writer is bound by
-// its instructions and takes no more than 16 channels a thread (8191 x 8 heads of 128: 13.4 us, two tokens 14.4); the
-// reader by what it has in flight, 32 (32768 x 16 heads of 64: 32.3 us with four tokens, 37.7 with two, 38.6 with one).
+// Tokens a thread once that still gives every SM eight blocks of threads; else one (latency).  The writer is a
+// chain of load, reduction and store, best with 16 channels a thread and many threads (8191 x 8 heads of 128: 13.4 us, two
+// tokens a thread 14.4); the reader needs loads in flight, 32 channels (32768 x 16 heads of 64: 32.3 us with four tokens, 37.7 with two, 38.6 with one).
 template <int G, bool WRITES>
 constexpr int kTokOf = (WRITES ? 2 : 4) / G;
 template <int G, bool WRITES>

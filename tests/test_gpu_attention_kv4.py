@@ -401,3 +401,59 @@ def test_long_prompts(n, L, D):
     ref, _, bound, _ = attention_ref(qs, one, table, [L], [n], D ** -0.5)
     assert_attention(x[:, :1], ref, bound)
     assert torch.equal(x, x[:, :1].expand(-1, 160, -1))
+
+
+@pytest.mark.parametrize("new", [[3, 4, 1, 2, 4], [4, 0, 4, 4, 3], [1, 3, 3, 5, 4], [2, 1, 1, 2, 2]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_ragged_drafts(new, D):
+    """Sequences of a few tokens each, one of them with more rows than the others' kernel takes; idle ones between."""
+    lens = [700, 33, 3, 5000, 64]
+    _run(lens, new, 8, 2, D, 16, F16, seed=sum(new))
+    _run(lens, new, 8, 2, D, 64, BF16, seed=sum(new), window=100)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [[1, 40, 1], [1, 300, 300], [20, 20, 20]])
+def test_prompts_and_tokens_in_one_call_follow_what_came_before(new, D):
+    """The two kernels of a ragged call overlap: neither starts before the cache's writer, nor does a later kernel
+    start before both."""
+    q = qg()
+    lens, P, H, Hq = [3000, 600, 900], 16, 2, 8
+    table, pages = paged(lens, P, 0)
+    T = sum(new)
+    tb, n = torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    slots = torch.arange(pages * P, device="cuda")
+    ks = [torch.randn(pages * P, H, D, device="cuda").to(F16) for _ in range(4)]
+    qs = torch.randn(T, Hq, D, device="cuda").to(F16)
+    want = []
+    for k in ks:
+        cache = q.kv4_cache(pages, H, D, P)
+        q.quantize_kv4(k, k, cache, slots)
+        torch.cuda.synchronize()
+        want.append(q.attention_kv4(qs, cache, tb, n, q_starts=starts))
+        torch.cuda.synchronize()
+    cache = q.kv4_cache(pages, H, D, P)
+    out = [torch.empty_like(qs) for _ in ks]
+    codes = [torch.empty(T, Hq * D, dtype=torch.int8, device="cuda") for _ in ks]
+    scales = [torch.empty(T, device="cuda") for _ in ks]
+
+    def step():
+        for i, k in enumerate(ks):
+            q.quantize_kv4(k, k, cache, slots)
+            q.attention_kv4(qs, cache, tb, n, q_starts=starts, out=out[i])
+            q.quantize_rowwise_int8(out[i].view(T, -1), out=codes[i], scale_out=scales[i])
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(20):
+        for o in out:
+            o.zero_()
+        graph.replay()
+        for i in range(len(ks)):
+            assert torch.equal(out[i], want[i])
+            a, b = q.quantize_rowwise_int8(want[i].view(T, -1))
+            assert torch.equal(codes[i], a) and torch.equal(scales[i], b)
+    q.check_device_errors()
