@@ -79,7 +79,7 @@ constexpr float kAhead = 8.0f;  // log2 of how far a score may pass the maximum 
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // fp16x2: -8 2^-24, -128 2^-24
 
 // device status sites
-enum : uint32_t { kSiteSequence = 1, kSitePage = 2, kSiteWait = 3 };
+enum : uint32_t { kSiteSequence = 1, kSitePage = 2, kSiteWait = 3, kSiteCopy = 4 };
 
 __device__ __forceinline__ void report(uint32_t code, uint32_t site) {
   atomicCAS(&g_status_attn, 0ull,
@@ -324,6 +324,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
       page = a.table[(int64_t)fill.b * a.table_ld + i];
       if (page < 0 || page >= a.cache.pages) {
         report(kDevBadArg, kSitePage);
+        page = -1;
+      } else if (!dcheck(in_area(in_page, piece, P) && in_area(dst_off, bytes, kStage) && (dst_off | bytes) % 16 == 0,
+                         &g_status_attn, kSiteCopy)) {
         page = -1;
       }
     }

@@ -86,7 +86,7 @@ constexpr float kLift = 7.0f, kAhead = 8.0f;
 
 enum : uint32_t {
   kSiteSequence = 1, kSitePage, kSiteRawFull, kSiteRawEmpty, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty,
-  kSiteS, kSiteP, kSiteO, kSiteQ, kSiteDrain
+  kSiteS, kSiteP, kSiteO, kSiteQ, kSiteDrain, kSiteCopy
 };
 
 __device__ __forceinline__ void report(uint32_t code, uint32_t site) {
@@ -422,6 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           page = __ldg(a.table + (int64_t)job.b * a.table_ld + pi);
           if (page < 0 || page >= a.cache.pages) {
             report(kDevBadArg, kSitePage);
+            page = -1;
+          } else if (!dcheck(in_area(in_page, piece, P) && in_area(dst_off, bytes, stage_bytes) && (dst_off | bytes) % 16 == 0,
+                             &g_status_prompt, kSiteCopy)) {
             page = -1;
           }
         }
