@@ -18,8 +18,8 @@
 // s kappa near 2^4 at p = 1, 2^18 above the first fp16 subnormal.  Codes are
 // taken from their middle because values have either sign: without it the sum
 // over n keys is large against the result and its truncation shows (0.0013
-// relative error at 131071 keys).  The product does it: half of its depth takes
-// 8 tokens' codes, the other half -8 for the same probabilities.
+// relative error at 131071 keys): an exact fp16 addition of -8 2^-24 to each
+// pair.
 //
 // mma.m16n8k16 with keys (16 tokens) or channels (16 of V^T) as its rows and up
 // to 8 query rows as its columns: the accumulators of q.c and of the output
@@ -30,11 +30,14 @@
 // 32 keys pass it by 8 binary digits: a vote instead of a reduction, and 32 keys
 // at a time keep a warp's state small.
 //
-// Measured, 64 sequences of 4096..8192 tokens, 64/8 heads of 128: 126 us, HBM's
-// rate is 70.  16 keys of 128 channels are about 280 instructions of a warp, 170
-// of them on the ALU (2 cycles each: masks, shifts, minima) and 24 products of 8
-// cycles; an SM sub-core takes 620 cycles, three warps deep in dependent chains.
-// About 12 us of a call are its beginning and end (lengths, first loads, joins).
+// Measured, 64 sequences of 4096..8192 tokens, 64/8 heads of 128: 119 us, HBM's
+// rate is 70.  A product takes the sub-core's issue for 8 cycles, in which no
+// other instruction goes out (probe: 8 products and 32 logic operations take 99
+// cycles, 64 and 64 alone), so 16 keys of 128 channels cost 16 products x 8 and
+// about 290 others, 170 of them on the half-rate ALU (masks, shifts, minima).
+// That is why the middle is an addition and not the other half of the products'
+// depth (24 products: 126 us).  About 12 us of a call are its beginning and end
+// (lengths, first loads, joins).
 //
 // Every warp is a worker of its own: the chunks of tokens of all sequences
 // and heads form one list, split evenly over the warps of one CTA per SM, so
@@ -68,15 +71,15 @@ unsigned long long read_clear_status_attn(cudaStream_t s) {
 namespace {
 
 // The ring: 64 tokens a stage and 2 stages for each of 12 warps (221 KB at 128 channels, the registers' 168 a thread).
-// 64 sequences of 4096..8192 tokens, 64/8 heads of 128: 126 us (3.6 TB/s); 8 or 10 warps 138, 147; stages of 32 tokens
-// 141.  Heads of 64 take 128 registers: 16 warps 83 us, 12 warps 89.  Two row tiles take 205 and more: 2 x 131071
-// tokens, 4 new ones, 32/8 heads of 64: 80 us with 8 warps, 81 with 12.
+// 64 sequences of 4096..8192 tokens, 64/8 heads of 128: 119 us (3.8 TB/s); 8 or 10 warps were 13 and 22 longer, stages
+// of 32 tokens 16.  Heads of 64 take 128 registers: 16 warps 81 us, 12 warps 6 more.  Two row tiles take 205 and more: 2 x
+// 131071 tokens, 4 new ones, 32/8 heads of 64: 73 us with 8 warps, not less with 12.
 constexpr int kChunk = 64;   // tokens per ring stage
 template <int G, int NT>
 constexpr int kWarpsOf = NT == 2 ? 8 : G == 1 ? 16 : 12;  // workers per CTA (registers: 65536 / (32 workers))
 constexpr int kStages = 2;
 constexpr float kAhead = 8.0f;  // log2 of how far a score may pass the maximum it is taken against
-constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // fp16x2: -8 2^-24, -128 2^-24
+constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // fp16x2: -8 2^-24, -128 2^-24 (16 codes' middle)
 
 // device status sites
 enum : uint32_t { kSiteSequence = 1, kSitePage = 2, kSiteWait = 3, kSiteCopy = 4 };
@@ -107,6 +110,12 @@ __device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t add_halves(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -717,17 +726,15 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
               const uint32_t sel = half ? 0x7632u : 0x5410u;
               const uint32_t e0 = __byte_perm(v0[0][g], v1[0][g], sel), e1 = __byte_perm(v0[1][g], v1[1][g], sel);
               const uint32_t f0 = e0 >> 8, f1 = e1 >> 8;
+              // codes from their middle, exact
+              const uint32_t a0 = add_halves(e0 & 0x000F000Fu, kMinus8), a1 = add_halves(f0 & 0x000F000Fu, kMinus8);
+              const uint32_t a2 = add_halves(e1 & 0x000F000Fu, kMinus8), a3 = add_halves(f1 & 0x000F000Fu, kMinus8);
+              const uint32_t b0 = add_halves(e0 & 0x00F000F0u, kMinus128), b1 = add_halves(f0 & 0x00F000F0u, kMinus128);
+              const uint32_t b2 = add_halves(e1 & 0x00F000F0u, kMinus128), b3 = add_halves(f1 & 0x00F000F0u, kMinus128);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                // the first 8 tokens: their codes, and -8 for the same probabilities; then the others
-                mma16816(o[nt][g][2 * half], e0 & 0x000F000Fu, f0 & 0x000F000Fu, kMinus8, kMinus8, pf[nt][g][0],
-                         pf[nt][g][0]);
-                mma16816(o[nt][g][2 * half], e1 & 0x000F000Fu, f1 & 0x000F000Fu, kMinus8, kMinus8, pf[nt][g][1],
-                         pf[nt][g][1]);
-                mma16816(o[nt][g][2 * half + 1], e0 & 0x00F000F0u, f0 & 0x00F000F0u, kMinus128, kMinus128, pf[nt][g][0],
-                         pf[nt][g][0]);
-                mma16816(o[nt][g][2 * half + 1], e1 & 0x00F000F0u, f1 & 0x00F000F0u, kMinus128, kMinus128, pf[nt][g][1],
-                         pf[nt][g][1]);
+                mma16816(o[nt][g][2 * half], a0, a1, a2, a3, pf[nt][g][0], pf[nt][g][1]);
+                mma16816(o[nt][g][2 * half + 1], b0, b1, b2, b3, pf[nt][g][0], pf[nt][g][1]);
               }
             }
           }

@@ -852,8 +852,8 @@ int64_t row_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
 
 // Rows (query tokens x head group) that the decode kernel takes, in tiles of 8; 0: none.  A ragged call gives it
 // the sequences of 8 rows at most, or of 16 where one token has more than 8 or the mean sequence has 9 to 16 (drafts;
-// 64 sequences of 4096..8192 tokens, 32/8 heads of 128, 60 of them with 3 new tokens: 213 us, 488 with the prompt kernel for
-// these; but one of them with 3: 202, 156 with the prompt kernel for it).
+// 64 sequences of 4096..8192 tokens, 32/8 heads of 128, 60 of them with 3 new tokens: 194 us, 488 with the prompt kernel for
+// these; but one of them with 3: 184, 149 with the prompt kernel for it).
 int decode_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
   int64_t rows = T / B * group;
   if (ragged) rows = T * group > 8 * B && T * group <= 16 * B ? 16 : group;
