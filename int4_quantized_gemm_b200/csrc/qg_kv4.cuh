@@ -63,11 +63,12 @@ struct Attn4 {
 
 #ifdef __CUDACC__
 // A sequence's query tokens [first, first + n) and its length, held to what
-// the arguments cover; false if the device data had to be cut.
+// the arguments cover; false if the device data had to be cut.  (Plain loads: a
+// fence in front of them orders them, where a kernel starts without a wait.)
 __device__ __forceinline__ bool attn4_sequence(const Attn4& a, int b, int& first, int& n, int& len) {
   bool ok = true;
   if (a.q_starts) {
-    const int s0 = __ldg(a.q_starts + b), s1 = __ldg(a.q_starts + b + 1);
+    const int s0 = a.q_starts[b], s1 = a.q_starts[b + 1];
     ok = s0 >= 0 && s1 >= s0 && s1 <= a.T;
     first = s0;
     n = ok ? s1 - s0 : 0;
@@ -75,7 +76,7 @@ __device__ __forceinline__ bool attn4_sequence(const Attn4& a, int b, int& first
     first = b * a.n_uniform;
     n = a.n_uniform;
   }
-  len = __ldg(a.seq_lens + b);
+  len = a.seq_lens[b];
   const int64_t room = (int64_t)a.max_pages * a.cache.page_size;
   if (len < 0 || len > room) {
     ok = false;

@@ -457,3 +457,41 @@ def test_prompts_and_tokens_in_one_call_follow_what_came_before(new, D):
             a, b = q.quantize_rowwise_int8(want[i].view(T, -1))
             assert torch.equal(codes[i], a) and torch.equal(scales[i], b)
     q.check_device_errors()
+
+
+@pytest.mark.parametrize("new", [[1, 1, 40, 1], [3, 4, 4, 3], [1, 300, 1, 1]])
+def test_ragged_calls_see_lengths_and_tables_written_just_before(new):
+    """Lengths, starts and table change on the device right before each call of a replayed graph."""
+    q = qg()
+    B, P, H, Hq, D, pages, calls = len(new), 16, 2, 8, 128, 600, 6
+    cache = random_cache(q, pages, H, D, P, 0)
+    rng = np.random.default_rng(0)
+    qs = torch.randn(sum(new), Hq, D, device="cuda").to(F16)
+    tables = [torch.from_numpy(rng.permutation(pages)[:B * 100].reshape(B, 100).astype(np.int32)).cuda() for _ in range(calls)]
+    lens = [torch.from_numpy(rng.integers(max(new), 1600, B).astype(np.int32)).cuda() for _ in range(calls)]
+    orders = [rng.permutation(new) for _ in range(calls)]
+    starts = [torch.tensor(np.concatenate([[0], np.cumsum(o)]), dtype=torch.int32, device="cuda") for o in orders]
+    want = []
+    for i in range(calls):
+        want.append(q.attention_kv4(qs, cache, tables[i], lens[i], q_starts=starts[i]))
+        torch.cuda.synchronize()
+    t, n, s = (torch.empty_like(x[0]) for x in (tables, lens, starts))
+    outs = [torch.empty_like(qs) for _ in range(calls)]
+
+    def step():
+        for i in range(calls):
+            t.copy_(tables[i])
+            s.copy_(starts[i])
+            n.copy_(lens[i])
+            q.attention_kv4(qs, cache, t, n, q_starts=s, out=outs[i])
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(30):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    q.check_device_errors()
