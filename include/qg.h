@@ -589,8 +589,8 @@ qg_status qg_dequantize_kv4(const qg_kv4_cache *cache, const int64_t *slots, voi
  * A query that sees nothing gives zeros (and lse = -inf).  Scores, sums and
  * outputs are held in binary32.  For the tensor cores are rounded to fp16: with
  * few query tokens the probabilities times the values' scale, with many the
- * probabilities and the dequantized keys and values.  A NaN or infinity in the
- * params of a key or value reaches the queries that see its token, no others.
+ * probabilities and the dequantized keys and values.  A NaN in the params of a
+ * key or value reaches the queries that see its token, no others.
  *
  *   q          [in]  device, [T, heads_q, head_dim] of dtype (QG_F16 or
  *              QG_BF16); strides in elements, multiples of 8.  heads_q is a
