@@ -23,7 +23,7 @@
 //
 // Roundings to fewer than 32 bits, all to fp16 because the tensor cores take two
 // 16-bit operands: queries (exact for fp16; bf16 has fewer digits and is scaled
-// into fp16's range), a key's and a value's c s + o, and p.  Each is half a step
+// into fp16's range, each row by its own power of two), a key's and a value's c s + o, and p.  Each is half a step
 // of 2^-11; scores, maxima, sums and outputs are binary32.  (At 2 x 4096 tokens
 // of fp16 they make 0.00037 of relative error beside the output's own rounding
 // of 0.00021: keys 0.00027, values 0.00020, p 0.00015.  Splitting keys into two
@@ -260,6 +260,9 @@ struct Layout {
   static constexpr uint32_t bytes = values + kRaw * kValueStage;
 };
 
+// The softmax warps wait for the exponents that the warps of the values' dequantization take.
+__device__ __forceinline__ void exponents_barrier() { named_barrier(1, 256 + 128); }
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -331,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t raw_full[2][kRaw], raw_empty[2][kRaw], k_full[kBuf], k_empty[kBuf],
       v_full[kBuf], v_empty[kBuf], s_full[2][2], p_full[2][2], o_done[2][2], q_full[2], drained;
   __shared__ uint32_t tmem_slot;
+  __shared__ int q_exp[kRows];  // of the power of two that a row of bf16 queries is scaled by
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smp = smem_raw + (sm - smem_u32(smem_raw));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -518,6 +522,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_down<kDequantRegs>();
     // ---- values to fp16: a lane takes one word (8 channels) of 8 tokens and writes 8 tokens of 8 channels ----
     const int dt = tid - 32 * kValueWarp;
+    if (a.dtype != QG_F16) {
+      // The exponents of the rows' scales, while there are no values yet: a row's own, so that a NaN or a large query
+      // does not cost the other rows digits.  (The softmax warps' own reduction took 6 to 13 % of the time of long
+      // prompts: registers of their loop went to it.)
+#pragma unroll 1
+      for (int r = dt; r < kRows; r += 128) {
+        const int row = row0 + r;
+        uint32_t most = 0;  // of the magnitudes' bits
+        if (row < job.rows) {
+          const uint4* p = reinterpret_cast<const uint4*>(
+              static_cast<const char*>(a.q) +
+              2 * ((job.first + row / a.group) * a.q_st + (job.h * a.group + row % a.group) * a.q_sh));
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) {
+            const uint4 x = __ldg(p + k);
+            const auto larger = [](uint32_t w) { return max(w << 16 & 0x7FFF0000u, w & 0x7FFF0000u); };
+            most = max(most, max(max(larger(x.x), larger(x.y)), max(larger(x.z), larger(x.w))));
+          }
+        }
+        q_exp[r] = max(-100, min(100, 8 - ((int)(most >> 23) - 127)));
+      }
+      exponents_barrier();
+    }
     const int jw = dt & 7, g = G == 2 ? dt >> 3 & 1 : 0, tg = dt >> (G == 2 ? 4 : 3);
     const int swap = tg & 1;  // odd groups read their pairs the other way round: no bank twice
     const uint32_t sel_lo = swap ? 0x1054u : 0x5410u, sel_hi = swap ? 0x3276u : 0x7632u;
@@ -660,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t place = sm + L::q + tile * L::kOperand + (piece / 8) * L::kBlock;  // of the lane's 16 bytes in row 0
     const auto in_row = [&](int r) { return place + (wrow + r) * 128 + (((piece & 7) ^ (r & 7)) << 4); };
-    // queries to fp16: as they are, or (bf16) scaled by a power of two that brings the warp's largest near 2^8
+    // queries to fp16: as they are, or (bf16) scaled by the power of two that brings the row's largest near 2^8
     float sigma = a.scale * 1.44269504088896f;
     if (a.dtype == QG_F16) {
 #pragma unroll
@@ -668,20 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         sts128(in_row(it * kRpi + sub), __byte_perm(qv[it].x, qv[it].z, 0x5410), __byte_perm(qv[it].x, qv[it].z, 0x7632),
                __byte_perm(qv[it].y, qv[it].w, 0x5410), __byte_perm(qv[it].y, qv[it].w, 0x7632));
     } else {
-      uint32_t most = 0;  // of the magnitudes' bits
+      exponents_barrier();  // they are there
+      sigma *= __uint_as_float((uint32_t)(127 - q_exp[tile * 128 + wrow + lane]) << 23);
 #pragma unroll
       for (int it = 0; it < kLpr; ++it) {
         const uint32_t* w = &qv[it].x;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) most = max(most, max(w[k] << 16 & 0x7FFF0000u, w[k] & 0x7FFF0000u));
-      }
-      most = __reduce_max_sync(0xffffffffu, most);
-      const int e = max(-100, min(100, 8 - ((int)(most >> 23) - 127)));
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      sigma *= __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-      for (int it = 0; it < kLpr; ++it) {
-        const uint32_t* w = &qv[it].x;
+        const float up = __uint_as_float((uint32_t)(127 + q_exp[tile * 128 + wrow + it * kRpi + sub]) << 23);
         const auto pair = [&](int i, int k) {  // values i and k
           const float x = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
           const float y = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
