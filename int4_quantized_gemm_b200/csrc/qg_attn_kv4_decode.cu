@@ -160,7 +160,7 @@ __device__ __forceinline__ Seq sequence(const Attn4& a, int b, bool& ok) {
   Seq s;
   ok = attn4_sequence(a, b, s.first, s.n, s.len);
   // the oldest key that any query sees
-  s.lo = a.window > 0 ? max(0, min(s.len, s.len - s.n - a.window + 1)) : 0;
+  s.lo = attn4_oldest(a, s.len - s.n);
   s.c0 = s.lo / kChunk;
   s.chunks = s.n == 0 || s.n > 8 * NT / a.group ? 0 : max(1, (s.len + kChunk - 1) / kChunk - s.c0);
   return s;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
         const int col = nt * 8 + 2 * q4 + c;
         const int pos = s.len - s.n + min(col, rows - 1) / a.group;
         end[nt][c] = a.causal ? min(s.len, pos + 1) : s.len;
-        beg[nt][c] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+        beg[nt][c] = attn4_oldest(a, pos);
       }
 #pragma unroll
       for (int g = 0; g < G; ++g)

@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int row0 = job.tile * kRows;
   const auto pos_of = [&](int row) { return job.len - job.n + row / a.group; };
   const auto end_of = [&](int row) { return max(0, a.causal ? min(job.len, pos_of(row) + 1) : job.len); };
-  const auto beg_of = [&](int row) { return a.window > 0 ? max(0, pos_of(row) - a.window + 1) : 0; };
+  const auto beg_of = [&](int row) { return attn4_oldest(a, pos_of(row)); };
   const int step0 = min(beg_of(row0), job.len) / kKeys;
   int steps[2];
 #pragma unroll

@@ -84,6 +84,12 @@ __device__ __forceinline__ bool attn4_sequence(const Attn4& a, int b, int& first
   }
   return ok;
 }
+
+// The oldest key that a query at `pos` sees.  (It may stand before the sequence, where pos - window + 1 can leave 32
+// bits: any such place gives 0.)
+__device__ __forceinline__ int attn4_oldest(const Attn4& a, int pos) {
+  return a.window > 0 ? max(0, max(pos, -1) - a.window + 1) : 0;
+}
 #endif
 
 }  // namespace qg
