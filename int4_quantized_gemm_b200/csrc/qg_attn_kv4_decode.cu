@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
       int e = 8 - ((int)(__float_as_uint(amax) >> 23) - 127);
       e = max(-100, min(100, e));
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      const float sg = a.scale * 1.44269504088896f * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23);
+      // (not zero, which would make a NaN of the first maximum's -inf)
+      const float sg =
+          fmaxf(a.scale * 1.44269504088896f * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23), 0x1p-126f);
       float sum[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {

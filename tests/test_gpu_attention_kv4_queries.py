@@ -1,5 +1,5 @@
 """Queries of any size in attention over the 4-bit cache: what one row holds does not
-reach the others."""
+reach the others, and rows without a score to speak of weigh every key alike."""
 from __future__ import annotations
 
 import numpy as np
@@ -66,3 +66,16 @@ def test_rows_of_very_different_sizes(D, n):
     one = sizes == 1.0
     assert one.any() and not one.all()
     assert_close(got[one], ref[one], bound[one])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n", [1, 4, 40])
+@pytest.mark.parametrize("scale", [1e-20, 1e-30, 1e-37])
+def test_zero_and_small_queries_with_a_small_scale(dtype, n, scale):
+    """Every visible key has the same weight."""
+    call, kv = setup(64)
+    qs = queries(n, 64, dtype)
+    qs[:, ::2] = 0
+    qs[:, 1] *= 2.0 ** -10
+    ref, _, bound, _ = exact(qs, kv, [n], scale)
+    assert_close(call(qs, scale=scale), ref, bound)
