@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
   float qs[NT][2][G];              // sums of the group's queries, times 2^-24: columns 2 q4, 2 q4 + 1
   float sigma[NT][2];              // scale log2(e) 2^24 over the queries' power of two
   float m[NT][2], l[NT][2];        // the maximum that scores are taken against (before sigma), and the sum
-  float mneg[NT][2];               // lift - m sigma; +inf: no key seen, so that the first one sets m
+  uint32_t unseen = 0;             // bit 2 nt + c: no key seen yet, m is 0
+  bool fresh = false;              // any column of the warp is such
   float ob[NT][2][G];              // sum p o
   float o[NT][G][4][4];            // sum p s (c - 8) 2^-24
   int end[NT][2], beg[NT][2];      // visible keys of the columns
@@ -403,11 +404,12 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // largest query near 2^8: exact in fp16 down to 2^-22 of it, also after the 1/16
       int e = 8 - ((int)(__float_as_uint(amax) >> 23) - 127);
-      e = max(-100, min(100, e));
+      e = max(-120, min(100, e));
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      // (not zero, which would make a NaN of the first maximum's -inf)
-      const float sg =
-          fmaxf(a.scale * 1.44269504088896f * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23), 0x1p-126f);
+      // (not zero, which would make a NaN of a hidden score, and not so large that a score, 2^8 at most, leaves binary32:
+      // from here on all of the weight is on the best key anyway)
+      const float sg = fminf(
+          fmaxf(a.scale * 1.44269504088896f * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23), 0x1p-126f), 0x1p118f);
       float sum[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -436,8 +438,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
           qs[nt][c][g] = __shfl_sync(0xffffffffu, sum[g], from) * 5.9604644775390625e-8f;
           ob[nt][c][g] = 0.0f;
         }
-        m[nt][c] = -INFINITY;
-        mneg[nt][c] = INFINITY;
+        m[nt][c] = 0.0f;
         l[nt][c] = 0.0f;
         const int col = nt * 8 + 2 * q4 + c;
         const int pos = s.len - s.n + min(col, rows - 1) / a.group;
@@ -455,6 +456,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
     max_beg = a.window > 0 ? s.len - a.window : 0;
     lift = 0.0f;
     limit = 0;
+    unseen = (1u << (2 * NT)) - 1;
+    fresh = true;
     starts_item = use.c == 0;
   };
 
@@ -483,7 +486,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
         }
         const int row = nt * 8 + 2 * q4 + c;
         if (row >= rows) continue;
-        const float top = m[nt][c] * sigma[nt][c] - lift;  // log2 units; -inf: nothing seen
+        const float top = unseen >> (2 * nt + c) & 1 ? -INFINITY : m[nt][c] * sigma[nt][c] - lift;  // log2 units
         const int t = s.first + row / a.group, hq = use.h * a.group + row % a.group;
         const float inv = l[nt][c] == 0.0f ? 0.0f : 1.0f / l[nt][c];
 #pragma unroll
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
 #pragma unroll
         for (int i2 = 0; i2 < 2; ++i2) {
           const int tile = 2 * step + i2;
-          // scores
+          // scores, less the maximum (m sigma alone may be so large that its rounding passes the exponential's range)
           uint32_t kw[2][2 * G], pw[2][G];
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
             for (int g = 0; g < G; ++g) so[g] = half2_f32(pw[k >> 1][g]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float v = so[0].y * qs[nt][k & 1][0];
+              float v = fmaf(so[0].y, qs[nt][k & 1][0], -m[nt][k & 1]);
 #pragma unroll
               for (int g = 0; g < G; ++g) {
                 if (g > 0) v = fmaf(so[g].y, qs[nt][k & 1][g], v);
@@ -635,12 +638,12 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float v = x[i2][nt][k];
-              e[i2][nt][k] = kAll || v != -INFINITY ? fmaf(v, sigma[nt][k & 1], mneg[nt][k & 1]) : -INFINITY;
+              e[i2][nt][k] = fmaf(v, sigma[nt][k & 1], lift);
               far = fmaxf(far, e[i2][nt][k]);
             }
         }
         smax &= 0x7FFFu;  // fp16 bits order like the values (a scale is not negative)
-        if (__any_sync(0xffffffffu, far > lift + kAhead || smax > limit)) {
+        if (fresh || __any_sync(0xffffffffu, far > lift + kAhead || smax > limit)) {
           smax = min(__reduce_max_sync(0xffffffffu, smax), 0x7BFFu);
           float shift = lift;
           if (smax > limit) {  // scale times kappa in [2^3, 2^4), up to 2^6 before this is done again; p up to 2^8
@@ -653,18 +656,19 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float t = fmaxf(fmaxf(m[nt][c], fmaxf(x[0][nt][c], x[0][nt][2 + c])), fmaxf(x[1][nt][c], x[1][nt][2 + c]));
+              float t = fmaxf(fmaxf(x[0][nt][c], x[0][nt][2 + c]), fmaxf(x[1][nt][c], x[1][nt][2 + c]));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-              const float safe = t == -INFINITY ? 0.0f : t;
-              const float corr = ex2(fmaf(m[nt][c] - safe, sigma[nt][c], shift));
-              m[nt][c] = t;
-              const float mn = fmaf(-safe, sigma[nt][c], lift);
-              mneg[nt][c] = t == -INFINITY ? INFINITY : mn;
+              const uint32_t bit = 1u << (2 * nt + c);
+              const bool first = unseen & bit;
+              if (t > -INFINITY) unseen &= ~bit;
+              t = first ? (t > -INFINITY ? t : 0.0f) : fmaxf(t, 0.0f);
+              m[nt][c] += t;
+              const float corr = first ? 0.0f : ex2(fmaf(-t, sigma[nt][c], shift));
 #pragma unroll
               for (int i2 = 0; i2 < 2; ++i2)
 #pragma unroll
-                for (int k = c; k < 4; k += 2) e[i2][nt][k] = fmaf(x[i2][nt][k], sigma[nt][c], mn);
+                for (int k = c; k < 4; k += 2) e[i2][nt][k] = fmaf(x[i2][nt][k] - t, sigma[nt][c], lift);
               l[nt][c] *= corr;
 #pragma unroll
               for (int g = 0; g < G; ++g) {
@@ -676,6 +680,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
                 }
               }
             }
+          fresh = __any_sync(0xffffffffu, unseen != 0);
         }
 
         // probabilities (times kappa) and the second product

@@ -83,6 +83,7 @@ static_assert(256 * kSoftmaxRegs + 256 * kDequantRegs + 128 * kOtherRegs <= kThr
 // half of its time between the products, in waits whose barriers had long completed.)
 constexpr int kMmaWarp = 0, kLoadWarp = 2, kSoftmaxWarp = 4, kKeyWarp = 12, kValueWarp = 16;
 constexpr float kLift = 7.0f, kAhead = 8.0f;
+constexpr float kFarScore = 8192.0f;  // log2 units
 
 enum : uint32_t {
   kSiteSequence = 1, kSitePage, kSiteRawFull, kSiteRawEmpty, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty,
@@ -293,17 +294,23 @@ __device__ __forceinline__ float row_max(const uint32_t (&v)[2][32], int cb, int
   return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 }
 
-// Stores p = 2^(x sigma + mneg) of a row's scores x in fp16 over the first half of their columns; returns their sum.
+// Stores p = 2^((x - m) sigma + kLift) of a row's scores x in fp16 over the first half of their columns; returns their
+// sum.  kAll: every column, as 2^(x sigma + mneg), mneg = kLift - m sigma, whose rounding is 2^-11 at kFarScore; further
+// on it would show, and pass the exponential's range at last, so those rows take the other form.
 template <bool kAll>
-__device__ __forceinline__ float row_exp(const uint32_t (&v)[2][32], uint32_t ts, float sigma, float mneg, int cb, int ce) {
+__device__ __forceinline__ float row_exp(const uint32_t (&v)[2][32], uint32_t ts, float sigma, float m, float mneg, int cb,
+                                         int ce) {
+  const auto power = [&](uint32_t bits) {
+    const float x = __uint_as_float(bits);
+    return kAll ? ex2(fmaf(x, sigma, mneg)) : ex2(fmaf(x - m, sigma, kLift));
+  };
   float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     uint32_t p[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float x = ex2(fmaf(__uint_as_float(v[c][2 * i]), sigma, mneg));
-      float y = ex2(fmaf(__uint_as_float(v[c][2 * i + 1]), sigma, mneg));
+      float x = power(v[c][2 * i]), y = power(v[c][2 * i + 1]);
       if constexpr (!kAll) {
         const int col = 32 * c + 2 * i;
         if (col < cb || col >= ce) x = 0.0f;
@@ -541,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             most = max(most, max(max(larger(x.x), larger(x.y)), max(larger(x.z), larger(x.w))));
           }
         }
-        q_exp[r] = max(-100, min(100, 8 - ((int)(most >> 23) - 127)));
+        q_exp[r] = max(-120, min(100, 8 - ((int)(most >> 23) - 127)));
       }
       exponents_barrier();
     }
@@ -709,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sts128(in_row(it * kRpi + sub), pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7));
       }
     }
+    sigma = fminf(sigma, 0x1p87f);  // scores, 2^39 at most, stay in binary32: by then the best key has all of the weight
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&q_full[tile]));
@@ -720,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int end = end_of(r), beg = beg_of(r);
     const int min_end = end_of(row0 + 128 * tile), max_beg = beg_of(last_row);
     float m = -INFINITY, mneg = 0.0f, l = 0.0f;  // the maximum taken against, kLift - m sigma, the sum of p 2^kLift
-    bool ok = true;
+    bool ok = true, far_scores = false;  // a row of the warp has a maximum beyond kFarScore
 #pragma unroll 1
     for (int j = 0; j < mine; ++j) {
       const uint32_t ts = tm_s + tile * 128 + (j & 1) * 64 + lanes;
@@ -741,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float corr = m == -INFINITY ? 0.0f : ex2((m - mn) * sigma);
         m = mn;
         mneg = m == -INFINITY ? 0.0f : fmaf(-m, sigma, kLift);
+        far_scores = __any_sync(0xffffffffu, fabsf(mneg) > kFarScore);
         l *= corr;
         if (j > 0) {
           // (of that barrier's phases all but this one are done: step j - 3's product came before step j - 1's scores)
@@ -758,7 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      l += full ? row_exp<true>(v, ts, sigma, mneg, cb, ce) : row_exp<false>(v, ts, sigma, mneg, cb, ce);
+      l += full && !far_scores ? row_exp<true>(v, ts, sigma, 0.0f, mneg, cb, ce)
+                               : row_exp<false>(v, ts, sigma, m == -INFINITY ? 0.0f : m, 0.0f, cb, ce);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(smem_u32(&p_full[tile][j & 1]));

@@ -1,13 +1,13 @@
 """Queries of any size in attention over the 4-bit cache: what one row holds does not
-reach the others, and rows without a score to speak of weigh every key alike."""
+reach the others, large and zero rows have their softmax's limit."""
 from __future__ import annotations
 
 import numpy as np
 import pytest
 import torch
 
-from kv4_sharp import assert_close, dequantised, exact
-from kv4_util import BF16, F16, paged, random_cache
+from kv4_sharp import U, assert_close, dequantised, exact
+from kv4_util import BF16, F16, half_step, paged, random_cache
 from parity_util import requires_cuda
 
 pytestmark = [pytest.mark.gpu, requires_cuda]
@@ -66,6 +66,31 @@ def test_rows_of_very_different_sizes(D, n):
     one = sizes == 1.0
     assert one.any() and not one.all()
     assert_close(got[one], ref[one], bound[one])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 4, 40])
+@pytest.mark.parametrize("size", [2.0 ** 80, 2.0 ** 118, 2.0 ** 124])
+def test_huge_queries_take_their_best_key(D, n, size):
+    """Scores so far apart that all of the weight is on one key, also where they pass binary32."""
+    call, kv = setup(D, offset=0.0)
+    qs = (queries(n, D, BF16).clamp(-7, 7).float() * size).to(BF16)
+    lse = torch.empty(n, 8, device="cuda")
+    got = call(qs, lse=lse).double()
+    k, v, _, r = kv[0]
+    some = 0
+    for h in range(8):
+        x = qs[:, h].double() @ k[h // 4].T * D ** -0.5
+        x = torch.where(torch.arange(L, device="cuda") <= torch.arange(L - n, L, device="cuda")[:, None], x, -torch.inf)
+        top = x.topk(2, 1)
+        spread = torch.sqrt(qs[:, h].double() ** 2 @ (k[h // 4] ** 2).T).amax(1) * D ** -0.5
+        clear = top.values[:, 0] - top.values[:, 1] > 20 * U * spread      # no rounding of a key changes the order
+        best = top.indices[:, 0]
+        # weight and value round to fp16 once each, the output to its type
+        allowed = (2 * U + 2 * half_step(BF16)) * (v[h // 4][best].abs() + r[h // 4][best])
+        assert ((got[:, h] - v[h // 4][best]).abs() <= allowed)[clear].all()
+        some += int(clear.sum())
+    assert some >= 4 * n
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
