@@ -15,7 +15,10 @@
 // by a power of two to fp16 (1/16 of it where they meet a nibble four bits up),
 // scale and offset enter per token and group in binary32.  p s is rounded to
 // fp16 under a power of two kappa (a shift of the running maximum) that keeps
-// s kappa near 2^4 at p = 1, 2^18 above the first fp16 subnormal.  Codes are
+// s kappa near 2^4 at p = 1, 2^18 above the first fp16 subnormal, for the largest
+// finite s that the row has seen: a later token's large or NaN scale costs no
+// row digits that does not see it (one kappa for all rows was 1.5 % faster with
+// one row tile, the same with two).  Codes are
 // taken from their middle because values have either sign: without it the sum
 // over n keys is large against the result and its truncation shows (0.0013
 // relative error at 131071 keys): an exact fp16 addition of -8 2^-24 to each
@@ -80,6 +83,10 @@ constexpr int kWarpsOf = NT == 2 ? 8 : G == 1 ? 16 : 12;  // workers per CTA (re
 constexpr int kStages = 2;
 constexpr float kAhead = 8.0f;  // log2 of how far a score may pass the maximum it is taken against
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;  // fp16x2: -8 2^-24, -128 2^-24 (16 codes' middle)
+
+// log2 kappa before any scale is known: that of the subnormal ones.  The largest scale (fp16 bits) that a kappa holds.
+constexpr float kLeastLift = 17.0f;
+__device__ __forceinline__ uint32_t scale_limit(float lift) { return min((uint32_t)(21.0f - lift) << 10, 0x7BFFu); }
 
 // device status sites
 enum : uint32_t { kSiteSequence = 1, kSitePage = 2, kSiteWait = 3, kSiteCopy = 4 };
@@ -365,8 +372,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
   float ob[NT][2][G];              // sum p o
   float o[NT][G][4][4];            // sum p s (c - 8) 2^-24
   int end[NT][2], beg[NT][2];      // visible keys of the columns
-  float lift = 0.0f;               // log2 kappa: l, ob and o hold p kappa
-  uint32_t limit = 0;              // largest scale (fp16 bits) that this kappa holds
+  float lift[NT][2];               // log2 kappa: l, ob and o hold p kappa
+  uint32_t limit = 0;              // largest scale (fp16 bits) that every column's kappa holds
   bool starts_item = false;
   int min_end = 0, max_beg = 0;    // keys that every row sees
 
@@ -439,6 +446,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
           ob[nt][c][g] = 0.0f;
         }
         m[nt][c] = 0.0f;
+        lift[nt][c] = kLeastLift;
         l[nt][c] = 0.0f;
         const int col = nt * 8 + 2 * q4 + c;
         const int pos = s.len - s.n + min(col, rows - 1) / a.group;
@@ -454,8 +462,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
     }
     min_end = a.causal ? s.len - s.n + 1 : s.len;
     max_beg = a.window > 0 ? s.len - a.window : 0;
-    lift = 0.0f;
-    limit = 0;
+    limit = scale_limit(kLeastLift);
     unseen = (1u << (2 * NT)) - 1;
     fresh = true;
     starts_item = use.c == 0;
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
         }
         const int row = nt * 8 + 2 * q4 + c;
         if (row >= rows) continue;
-        const float top = unseen >> (2 * nt + c) & 1 ? -INFINITY : m[nt][c] * sigma[nt][c] - lift;  // log2 units
+        const float top = unseen >> (2 * nt + c) & 1 ? -INFINITY : m[nt][c] * sigma[nt][c] - lift[nt][c];  // log2 units
         const int t = s.first + row / a.group, hq = use.h * a.group + row % a.group;
         const float inv = l[nt][c] == 0.0f ? 0.0f : 1.0f / l[nt][c];
 #pragma unroll
@@ -620,9 +627,11 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
           }
         }
 
-        // does a score pass the maximum too far, or a scale (of a key that any row sees) what kappa holds?
+        // does a score pass the maximum too far, or a scale (of a key that any row sees) what a kappa holds?
         uint32_t smax = 0;
-        float e[2][NT][4], far = -INFINITY;
+        float far[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) far[nt][0] = far[nt][1] = -INFINITY;
 #pragma unroll
         for (int i2 = 0; i2 < 2; ++i2) {
 #pragma unroll
@@ -636,39 +645,69 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float v = x[i2][nt][k];
-              e[i2][nt][k] = fmaf(v, sigma[nt][k & 1], lift);
-              far = fmaxf(far, e[i2][nt][k]);
-            }
+            for (int k = 0; k < 4; ++k) far[nt][k & 1] = fmaxf(far[nt][k & 1], x[i2][nt][k]);
         }
         smax &= 0x7FFFu;  // fp16 bits order like the values (a scale is not negative)
-        if (fresh || __any_sync(0xffffffffu, far > lift + kAhead || smax > limit)) {
-          smax = min(__reduce_max_sync(0xffffffffu, smax), 0x7BFFu);
-          float shift = lift;
-          if (smax > limit) {  // scale times kappa in [2^3, 2^4), up to 2^6 before this is done again; p up to 2^8
-            const uint32_t ex = max(smax >> 10, 1u);  // the scale's exponent, 15 for 1
-            lift = 18.0f - (float)ex;
-            limit = min((ex + 3) << 10, 0x7BFFu);
-          }
-          shift = lift - shift;
+        bool move = fresh || smax > limit;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) move |= far[nt][0] * sigma[nt][0] > kAhead || far[nt][1] * sigma[nt][1] > kAhead;
+        if (__any_sync(0xffffffffu, move)) {
+          // the tokens' largest scales; one that is not finite makes a NaN under any kappa
+          uint32_t scale[2][2], least = 0xFFFFFFFFu;
+#pragma unroll
+          for (int i2 = 0; i2 < 2; ++i2)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              scale[i2][hh] = 0;
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+                const uint32_t b = vw[i2][hh][g] & 0x7FFFu;
+                if (b < 0x7C00u) scale[i2][hh] = max(scale[i2][hh], b);
+              }
+            }
+          // the largest score and scale of the keys that each column's row sees (what others hold is nothing to it)
+          float best[NT][2];
+          uint32_t top[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float t = fmaxf(fmaxf(x[0][nt][c], x[0][nt][2 + c]), fmaxf(x[1][nt][c], x[1][nt][2 + c]));
-#pragma unroll
-              for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-              const uint32_t bit = 1u << (2 * nt + c);
-              const bool first = unseen & bit;
-              if (t > -INFINITY) unseen &= ~bit;
-              t = first ? (t > -INFINITY ? t : 0.0f) : fmaxf(t, 0.0f);
-              m[nt][c] += t;
-              const float corr = first ? 0.0f : ex2(fmaf(-t, sigma[nt][c], shift));
+              best[nt][c] = fmaxf(fmaxf(x[0][nt][c], x[0][nt][2 + c]), fmaxf(x[1][nt][c], x[1][nt][2 + c]));
+              top[nt][c] = 0;
 #pragma unroll
               for (int i2 = 0; i2 < 2; ++i2)
 #pragma unroll
-                for (int k = c; k < 4; k += 2) e[i2][nt][k] = fmaf(x[i2][nt][k] - t, sigma[nt][c], lift);
+                for (int hh = 0; hh < 2; ++hh)
+                  if (kAll || x[i2][nt][2 * hh + c] != -INFINITY) top[nt][c] = max(top[nt][c], scale[i2][hh]);
+            }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                best[nt][c] = fmaxf(best[nt][c], __shfl_xor_sync(0xffffffffu, best[nt][c], d));
+                top[nt][c] = max(top[nt][c], __shfl_xor_sync(0xffffffffu, top[nt][c], d));
+              }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t bit = 1u << (2 * nt + c);
+              const bool first = unseen & bit;
+              float t = fmaxf(best[nt][c], first ? -INFINITY : 0.0f);  // how far the maximum moves
+              if (t > -INFINITY) unseen &= ~bit;
+              else t = 0.0f;
+              m[nt][c] += t;
+              // scale times kappa in [2^3, 2^4), up to 2^6 before this is done again; p up to 2^8
+              const float old = lift[nt][c];
+              if (top[nt][c] > scale_limit(old)) lift[nt][c] = 18.0f - (float)(top[nt][c] >> 10);  // the scale's exponent, 15 for 1
+              least = min(least, scale_limit(lift[nt][c]));
+              const float corr = first ? 0.0f : ex2(fmaf(-t, sigma[nt][c], lift[nt][c] - old));
+#pragma unroll
+              for (int i2 = 0; i2 < 2; ++i2)
+#pragma unroll
+                for (int k = c; k < 4; k += 2) x[i2][nt][k] -= t;
               l[nt][c] *= corr;
 #pragma unroll
               for (int g = 0; g < G; ++g) {
@@ -681,6 +720,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
               }
             }
           fresh = __any_sync(0xffffffffu, unseen != 0);
+          limit = __reduce_min_sync(0xffffffffu, least);
         }
 
         // probabilities (times kappa) and the second product
@@ -701,7 +741,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
               float p[2];
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                p[c] = ex2(e[i2][nt][2 * hh + c]);
+                p[c] = ex2(fmaf(x[i2][nt][2 * hh + c], sigma[nt][c], lift[nt][c]));
                 l[nt][c] += p[c];
               }
 #pragma unroll
