@@ -230,7 +230,7 @@ __device__ __forceinline__ void write_part(float* p, int row, int lane, float to
 
 template <int G, int NT>
 __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
-    attention_kv4_decode(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch, bool behind_prompts) {
+    attention_kv4_decode(const __grid_constant__ Attn4 a, const __grid_constant__ Scratch scratch) {
   constexpr int kWarps = kWarpsOf<G, NT>;
   constexpr int D = 64 * G;
   constexpr uint32_t kCodes = kChunk * D / 2, kParams = kChunk * G * 4;
@@ -254,11 +254,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
     fence_mbar_init();
   }
   pdl_trigger();
-  // Behind the prompt kernel of the same call this one works on the blocks' place as they leave: that kernel lets its
-  // dependents start once all of its blocks are past their own wait, and shares no output with this one.  The last
-  // block waits for it instead, so that what follows waits for both.
-  if (!behind_prompts) pdl_wait();
-  else __threadfence();
+  // (Also behind the prompt kernel of the same call, with which it shares nothing but its inputs: only this wait makes
+  // what earlier grids wrote visible.  Overlapped without it, 16 sequences of 4096 tokens, two with 512 new ones, took
+  // 111 instead of 121 us.)
+  pdl_wait();
 
   // prefix[b]: chunks (times heads) of the sequences before b
   const int per = (a.B + 32 * kWarps - 1) / (32 * kWarps);
@@ -798,7 +797,6 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
     if (i + 1 < units) use.next(a);
   }
 
-  if (behind_prompts && blockIdx.x == gridDim.x - 1) pdl_wait();
   // --- what the warps left unfinished -----------------------------------------
   // In list order: each warp's continued item, then the one it started.  A group of parts that belong together
   // begins with a started item (or the CTA's first part) and takes every continued one up to the item's end.
@@ -879,7 +877,7 @@ Scratch scratch_of(void* workspace) {
 }
 
 template <int G, int NT>
-qg_status launch(const Attn4& a, bool behind_prompts, void* workspace, cudaStream_t s) {
+qg_status launch(const Attn4& a, void* workspace, cudaStream_t s) {
   constexpr int D = 64 * G, kWarps = kWarpsOf<G, NT>;
   constexpr int kRing = kWarps * kStages * 2 * kChunk * (D / 2 + 4 * G);
   constexpr int kMost = kRing > 4097 * 4 ? kRing : 4097 * 4;  // the prefix of 4096 sequences shares the ring's place
@@ -892,7 +890,7 @@ qg_status launch(const Attn4& a, bool behind_prompts, void* workspace, cudaStrea
   const int grid = sm_count();
   const Scratch scratch = scratch_of<G, NT>(workspace);
   LaunchCfg lc((unsigned)grid, 32 * kWarps, kMost, s);
-  cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_decode<G, NT>, a, scratch, behind_prompts);
+  cudaError_t e = cudaLaunchKernelEx(&lc.cfg, attention_kv4_decode<G, NT>, a, scratch);
   return check_cuda(e, "attention_kv4 decode launch");
 }
 
@@ -910,10 +908,10 @@ size_t attention_kv4_decode_workspace(int64_t dim, int nt) {
   return crossing_bytes() + (size_t)sm_count() * ((nt == 2 ? kWarpsOf<2, 2> : dim == 64 ? kWarpsOf<1, 1> : kWarpsOf<2, 1>) + 1) * 2 * part_floats(nt, (int)dim) * sizeof(float);
 }
 
-qg_status launch_attention_kv4_decode(const Attn4& a, int nt, bool behind_prompts, void* workspace, cudaStream_t s) {
+qg_status launch_attention_kv4_decode(const Attn4& a, int nt, void* workspace, cudaStream_t s) {
   if (a.cache.dim == 64)
-    return nt == 1 ? launch<1, 1>(a, behind_prompts, workspace, s) : launch<1, 2>(a, behind_prompts, workspace, s);
-  return nt == 1 ? launch<2, 1>(a, behind_prompts, workspace, s) : launch<2, 2>(a, behind_prompts, workspace, s);
+    return nt == 1 ? launch<1, 1>(a, workspace, s) : launch<1, 2>(a, workspace, s);
+  return nt == 1 ? launch<2, 1>(a, workspace, s) : launch<2, 2>(a, workspace, s);
 }
 
 qg_status launch_attention_kv4_decode_join(const Attn4& a, int nt, void* workspace, cudaStream_t s) {

@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&drained), 2);
     fence_mbar_init();
   }
+  pdl_trigger();
   pdl_wait();
-  pdl_trigger();  // behind the wait: the decode kernel of a ragged call relies on it
   if (blockIdx.x == 0)
     for (int b = tid; b < a.B; b += kThreads) {
       int f, n, l;
@@ -957,7 +957,7 @@ size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t he
 }
 
 // Single tokens and drafts go to the decode kernel, longer ones here; a ragged call launches both and each takes its
-// sequences: first the prompts, then the others on the place that their blocks leave.
+// sequences, the prompts first.
 qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s) {
   const int nt = decode_tiles(a.B, a.T, a.group, a.q_starts != nullptr);
   const bool prompts = !nt || a.q_starts;
@@ -969,7 +969,7 @@ qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s) 
     st = n.parts ? launch<1, true>(a, min_rows, n, mine, s) : launch<1, false>(a, min_rows, n, mine, s);
   else if (prompts)
     st = n.parts ? launch<2, true>(a, min_rows, n, mine, s) : launch<2, false>(a, min_rows, n, mine, s);
-  if (st == QG_OK && nt) st = launch_attention_kv4_decode(a, nt, prompts, workspace, s);
+  if (st == QG_OK && nt) st = launch_attention_kv4_decode(a, nt, workspace, s);
   if (st == QG_OK && prompts && n.parts)
     st = a.cache.dim == 64 ? launch_join<1>(a, min_rows, n, mine, s) : launch_join<2>(a, min_rows, n, mine, s);
   if (st == QG_OK && nt) st = launch_attention_kv4_decode_join(a, nt, workspace, s);

@@ -198,7 +198,7 @@ qg_status launch_attention_kv4(const Attn4& a, void* workspace, cudaStream_t s);
 size_t attention_kv4_workspace(int64_t B, int64_t T, int64_t heads_q, int64_t heads, int64_t dim, bool ragged);
 unsigned long long read_clear_status_kv4(cudaStream_t s);
 // Sequences of at most 8 nt query rows per KV head (qg_attn_kv4_decode.cu).
-qg_status launch_attention_kv4_decode(const Attn4& a, int nt, bool behind_prompts, void* workspace, cudaStream_t s);
+qg_status launch_attention_kv4_decode(const Attn4& a, int nt, void* workspace, cudaStream_t s);
 qg_status launch_attention_kv4_decode_join(const Attn4& a, int nt, void* workspace, cudaStream_t s);
 size_t attention_kv4_decode_workspace(int64_t dim, int nt);
 unsigned long long read_clear_status_attn(cudaStream_t s);

@@ -63,8 +63,7 @@ struct Attn4 {
 
 #ifdef __CUDACC__
 // A sequence's query tokens [first, first + n) and its length, held to what
-// the arguments cover; false if the device data had to be cut.  (Plain loads: a
-// fence in front of them orders them, where a kernel starts without a wait.)
+// the arguments cover; false if the device data had to be cut.
 __device__ __forceinline__ bool attn4_sequence(const Attn4& a, int b, int& first, int& n, int& len) {
   bool ok = true;
   if (a.q_starts) {
