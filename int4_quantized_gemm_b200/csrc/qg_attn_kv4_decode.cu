@@ -557,8 +557,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
       }
     }
     if (new_item) begin_item();
-    if (!mbar_wait(smem_u32(&bars[warp][stage]), (phases >> stage) & 1, &g_status_attn, kSiteWait)) {
-      // give up: let the other copies in flight land (bounded), then leave
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[warp][stage]), (phases >> stage) & 1, &g_status_attn, kSiteWait))) {
+      // give up, all lanes together: let the other copies in flight land (bounded), then leave
       for (int k = 1; k < kStages && i + k < filled; ++k)
         mbar_wait(smem_u32(&bars[warp][(i + k) % kStages]), (phases >> ((i + k) % kStages)) & 1, &g_status_attn, kSiteWait);
       break;

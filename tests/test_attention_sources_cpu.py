@@ -24,3 +24,9 @@ def test_every_kernel_waits_for_what_came_before(name):
     assert kernels > 0
     plain = re.findall(r"^  pdl_wait\(\);", text, re.M)      # a statement of the kernel's own block
     assert len(plain) == len(re.findall(r"\bpdl_wait\(", text)) == kernels
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_a_wait_that_gives_up_does_so_for_the_whole_warp(name):
+    """A bounded wait ends lane by lane; what a warp does next is decided by all of its lanes."""
+    assert not re.findall(r"if \(!\s*mbar_wait\(", source(name))
