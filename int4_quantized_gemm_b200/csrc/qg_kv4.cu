@@ -147,7 +147,8 @@ __device__ __forceinline__ int64_t row_of(const KV4& cache, int64_t slot, int64_
   }
   const uint32_t page = slot < ((int64_t)1 << 35) ? kv4_page(cache, (uint32_t)(slot >> 4)) : (uint32_t)(slot / cache.page_size);
   const uint32_t in = (uint32_t)slot - page * (uint32_t)cache.page_size;
-  return (int64_t)((uint64_t)page * ((uint32_t)cache.heads * (uint32_t)cache.page_size)) + (h * cache.page_size + in);
+  return (int64_t)((uint64_t)page * ((uint32_t)cache.heads * (uint32_t)cache.page_size)) +
+         ((uint32_t)h * (uint32_t)cache.page_size + in);
 }
 
 template <int G>

@@ -165,9 +165,10 @@ __global__ void __launch_bounds__(THREADS* ROWS)
     }
   }
   // the last K % 8 elements, one per thread (THREADS >= 32 > 7)
-  const int kt = K / 8 * 8 + t;
+  const bool tail = t < K % 8;
+  const int kt = K / 8 * 8 + t % 8;
   float tail_p = 0.0f;
-  if (active && kt < K) {
+  if (active && tail) {
     float v = (float)xr[kt];
     if (rr) {
       const T s = (T)__fadd_rn(v, (float)rr[kt]);
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(THREADS* ROWS)
     const uint4* hv = rr ? reinterpret_cast<const uint4*>(orow) : xv;
     for (int i = t; i < nvec; i += THREADS) qv[i] = codes8<T>(hv[i], __ldg(wv + i), inv);
   }
-  if (kt < K) qrow[kt] = (int8_t)code1(tail_p, inv);
+  if (tail) qrow[kt] = (int8_t)code1(tail_p, inv);
   if (t == 0) {
     const float norm = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)K), eps)));
     xs[m] = finite ? __fmul_rn(__fdiv_rn(a, 127.0f), norm) : __int_as_float(0x7fffffff);
@@ -226,7 +227,7 @@ cudaError_t launch_norm(const void* x, int64_t ldx, const void* residual, int64_
                         int8_t* xq, int64_t ldq, float* xs, void* res_out, int64_t ldo, int M, int K,
                         cudaStream_t s) {
   auto go = [&](auto kernel, int threads, int rows) {
-    LaunchCfg lc((unsigned)((M + rows - 1) / rows), (unsigned)(threads * rows), 0, s);
+    LaunchCfg lc((unsigned)(((int64_t)M + rows - 1) / rows), (unsigned)(threads * rows), 0, s);
     return cudaLaunchKernelEx(&lc.cfg, kernel, static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr,
                               static_cast<const T*>(weight), eps, xq, ldq, xs, static_cast<T*>(res_out), ldo, M, K);
   };
@@ -287,7 +288,8 @@ __global__ void __launch_bounds__(128) dequantize_rowwise_kernel(const int8_t* _
                                                                  int64_t ldy, int M, int K) {
   pdl_trigger();
   pdl_wait();
-  const int nvec = K / 8, t = threadIdx.x, kt = nvec * 8 + t;
+  const int nvec = K / 8, t = threadIdx.x, kt = nvec * 8 + t % 8;
+  const bool tail = t < K % 8;
   if constexpr (BY_ROWS) {
     const int across = blockDim.x, down = blockDim.y;  // down: rows at a time
     const int64_t row0 = (int64_t)blockIdx.x * (VEC * down) + threadIdx.y;
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(128) dequantize_rowwise_kernel(const int8_t* _
       for (int j = 0; j < VEC; ++j)
         if (row0 + j * down < M) read8<T>(c[j], s[j], y + (row0 + j * down) * ldy + 8 * i);
     }
-    if (kt < K)
+    if (tail)
       for (int j = 0; j < VEC; ++j)
         if (row0 + j * down < M) y[(row0 + j * down) * ldy + kt] = (T)__fmul_rn((float)xq[(row0 + j * down) * ldq + kt], s[j]);
   } else {
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(128) dequantize_rowwise_kernel(const int8_t* _
         for (int j = 0; j < VEC; ++j)
           if (base + 128 * j < nvec) read8<T>(c[j], s, out + 8 * (base + 128 * j));
       }
-      if (blockIdx.y == 0 && kt < K) out[kt] = (T)__fmul_rn((float)q[kt], s);
+      if (blockIdx.y == 0 && tail) out[kt] = (T)__fmul_rn((float)q[kt], s);
     }
   }
 }
