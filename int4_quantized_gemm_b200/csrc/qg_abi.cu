@@ -813,7 +813,8 @@ qg_status qg_dequantize_kv4(const qg_kv4_cache* cache, const int64_t* slots, voi
 size_t qg_attention_kv4_workspace_size(int64_t B, int64_t T, int64_t heads_q, int64_t num_heads, int64_t head_dim,
                                        int ragged) {
   if (B <= 0 || T <= 0 || heads_q <= 0 || num_heads <= 0 || heads_q % num_heads != 0 ||
-      (head_dim != 64 && head_dim != 128) || T * heads_q >= kMaxDim)
+      (head_dim != 64 && head_dim != 128) || B > kMaxSequences || T >= kMaxDim || heads_q >= kMaxDim ||
+      T * heads_q >= kMaxDim)
     return 0;
   return attention_kv4_workspace(B, T, heads_q, num_heads, head_dim, ragged != 0);
 }
@@ -832,7 +833,7 @@ qg_status qg_attention_kv4(const void* q, int64_t q_stride_t, int64_t q_stride_h
   if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QG_ERR_INVALID_ARG, "scale %g is not a positive number", (double)scale);
   if (window < 0 || max_pages < 0) return fail(QG_ERR_INVALID_ARG, "negative window or max_pages");
   if (B > kMaxSequences) return fail(QG_ERR_UNSUPPORTED, "B=%lld sequences: at most %d", (long long)B, kMaxSequences);
-  if (T * heads_q >= kMaxDim || max_pages * a.cache.page_size >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "T * heads_q or max_pages * page_size >= 2^31");
+  if (T * heads_q >= kMaxDim || max_pages >= kMaxDim || max_pages * a.cache.page_size >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "T * heads_q or max_pages * page_size >= 2^31");
   if (B * a.cache.heads * (max_pages * a.cache.page_size / 64 + 1) >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "B * num_heads * max_pages * page_size / 64 >= 2^31");
   if (B > 0 && !q_starts && T % B != 0) return fail(QG_ERR_INVALID_ARG, "T=%lld is not a multiple of B=%lld (pass q_starts)", (long long)T, (long long)B);
   if (B == 0 || T == 0) return QG_OK;

@@ -1,0 +1,19 @@
+"""Sizes of attention over the 4-bit cache that its checks have to see through."""
+from __future__ import annotations
+
+import pytest
+
+from test_kv4_args_cpu import R, U, attend, cache
+
+
+@pytest.mark.parametrize("page", [16, 64, 65536])
+@pytest.mark.parametrize("power", [31, 32, 48, 58, 60, 62])
+def test_tables_whose_tokens_leave_64_bits_are_refused(page, power):
+    """max_pages * page_size may be 0 in 64 bits."""
+    assert attend(c=cache(page=page), pages=1 << power, ld=1 << power) == U
+
+
+def test_no_workspace_for_calls_that_are_refused():
+    f = R.qg_attention_kv4_workspace_size
+    assert f(1, 1 << 40, 1 << 40, 1, 64, 0) == 0 and f(4097, 4097, 4, 2, 64, 0) == 0 and f(1, 1 << 31, 1, 1, 64, 1) == 0
+    assert f(2, 1 << 33, 1 << 31, 1, 64, 1) == 0
