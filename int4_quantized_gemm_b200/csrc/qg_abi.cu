@@ -835,7 +835,7 @@ qg_status qg_attention_kv4(const void* q, int64_t q_stride_t, int64_t q_stride_h
   if (B > kMaxSequences) return fail(QG_ERR_UNSUPPORTED, "B=%lld sequences: at most %d", (long long)B, kMaxSequences);
   if (T * heads_q >= kMaxDim || max_pages >= kMaxDim || max_pages * a.cache.page_size >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "T * heads_q or max_pages * page_size >= 2^31");
   if (B * a.cache.heads * (max_pages * a.cache.page_size / 64 + 1) >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "B * num_heads * max_pages * page_size / 64 >= 2^31");
-  if (B > 0 && !q_starts && T % B != 0) return fail(QG_ERR_INVALID_ARG, "T=%lld is not a multiple of B=%lld (pass q_starts)", (long long)T, (long long)B);
+  if (!q_starts && (B > 0 ? T % B : T) != 0) return fail(QG_ERR_INVALID_ARG, "T=%lld is not a multiple of B=%lld (pass q_starts)", (long long)T, (long long)B);
   if (B == 0 || T == 0) return QG_OK;
   QG_TRY(check_rows3(q, q_stride_t, q_stride_h, 2, "q"));
   QG_TRY(check_rows3(out, out_stride_t, out_stride_h, 2, "out"));

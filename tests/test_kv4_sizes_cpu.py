@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import pytest
 
-from test_kv4_args_cpu import R, U, attend, cache
+from test_kv4_args_cpu import F, I, R, U, attend, cache
 
 
 @pytest.mark.parametrize("page", [16, 64, 65536])
@@ -11,6 +11,12 @@ from test_kv4_args_cpu import R, U, attend, cache
 def test_tables_whose_tokens_leave_64_bits_are_refused(page, power):
     """max_pages * page_size may be 0 in 64 bits."""
     assert attend(c=cache(page=page), pages=1 << power, ld=1 << power) == U
+
+
+def test_query_tokens_of_no_sequence_are_refused():
+    """Nothing would write their outputs; with starts they lie behind the last sequence and are left alone."""
+    assert attend(B=0, T=2) == I
+    assert attend(B=0, T=2, starts=F) == 0 and attend(B=0, T=0) == 0
 
 
 def test_no_workspace_for_calls_that_are_refused():
