@@ -175,6 +175,7 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxKInt8 = 133144;  // 2^31 / 127^2: int32 accumulation stays exact
 constexpr int kMaxSequences = 4096;    // per attention call: their lengths are scanned in shared memory
+constexpr int64_t kMaxTokens = kMaxDim - 128;  // of a sequence: the end of a step of 64 keys stays below 2^31
 constexpr int64_t kMaxKZp = 131071;    // 2^31 / 128^2 - 1: the same with codes in [-128, 127]
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -833,7 +834,7 @@ qg_status qg_attention_kv4(const void* q, int64_t q_stride_t, int64_t q_stride_h
   if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QG_ERR_INVALID_ARG, "scale %g is not a positive number", (double)scale);
   if (window < 0 || max_pages < 0) return fail(QG_ERR_INVALID_ARG, "negative window or max_pages");
   if (B > kMaxSequences) return fail(QG_ERR_UNSUPPORTED, "B=%lld sequences: at most %d", (long long)B, kMaxSequences);
-  if (T * heads_q >= kMaxDim || max_pages >= kMaxDim || max_pages * a.cache.page_size >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "T * heads_q or max_pages * page_size >= 2^31");
+  if (T * heads_q >= kMaxDim || max_pages >= kMaxDim || max_pages * a.cache.page_size > kMaxTokens) return fail(QG_ERR_UNSUPPORTED, "T * heads_q >= 2^31 or max_pages * page_size > 2^31 - 128");
   if (B * a.cache.heads * (max_pages * a.cache.page_size / 64 + 1) >= kMaxDim) return fail(QG_ERR_UNSUPPORTED, "B * num_heads * max_pages * page_size / 64 >= 2^31");
   if (!q_starts && (B > 0 ? T % B : T) != 0) return fail(QG_ERR_INVALID_ARG, "T=%lld is not a multiple of B=%lld (pass q_starts)", (long long)T, (long long)B);
   if (B == 0 || T == 0) return QG_OK;

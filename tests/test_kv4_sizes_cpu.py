@@ -2,7 +2,9 @@
 from __future__ import annotations
 
 import pytest
+import torch
 
+import int4_quantized_gemm_b200 as qg
 from test_kv4_args_cpu import F, I, R, U, attend, cache
 
 
@@ -11,6 +13,14 @@ from test_kv4_args_cpu import F, I, R, U, attend, cache
 def test_tables_whose_tokens_leave_64_bits_are_refused(page, power):
     """max_pages * page_size may be 0 in 64 bits."""
     assert attend(c=cache(page=page), pages=1 << power, ld=1 << power) == U
+
+
+def test_sequences_next_to_2_to_the_31_are_refused():
+    """The end of their last step would not fit in 32 bits."""
+    for page, pages in ((16, (1 << 27) - 1), (16, (1 << 27) - 7), (48, (1 << 31) // 48), (64, (1 << 25) - 1)):
+        assert attend(c=cache(page=page, heads=1), B=1, T=1, Hq=1, pages=pages, ld=pages) == U
+    if not torch.cuda.is_available():                 # (a device would run the call, whose pointers are made up)
+        assert attend(c=cache(page=16, heads=1), B=1, T=1, Hq=1, pages=(1 << 27) - 8, ld=1 << 27) == qg.QG_ERR_NO_DEVICE
 
 
 def test_query_tokens_of_no_sequence_are_refused():
