@@ -533,7 +533,8 @@ qg_status qg_dequantize_rowwise_int8(const int8_t *xq, int64_t ldxq, const float
  *   codes   word [j, g] of int32 [num_pages, num_heads, page_size, 8, head_dim/64]:
  *           channels 64 g + 8 j .. + 7, channel i of them in bits 4 i
  *   params  fp16 [num_pages, num_heads, page_size, head_dim/64, 2]: scale and
- *           offset of each group of 64 channels;  value = scale * code + offset
+ *           offset of each group of 64 channels;  value = scale * code + offset,
+ *           scale not negative
  * Arrays are dense and 16-byte aligned.  head_dim is 64 or 128, page_size a
  * multiple of 16 (QG_ERR_INVALID_ARG otherwise; other head_dim
  * QG_ERR_UNSUPPORTED).
@@ -588,9 +589,12 @@ qg_status qg_dequantize_kv4(const qg_kv4_cache *cache, const int64_t *slots, voi
  *   j <= its own (causal != 0), and  j > its own - window (window > 0).
  * A query that sees nothing gives zeros (and lse = -inf).  Scores, sums and
  * outputs are held in binary32.  For the tensor cores are rounded to fp16: with
- * few query tokens the probabilities times the values' scale, with many the
- * probabilities and the dequantized keys and values.  A NaN in the params of a
- * key or value reaches the queries that see its token, no others.
+ * few query tokens the probabilities times the values' scale (to 2^-11 of it, or
+ * 2^-25 of the largest scale that the query sees), with many the probabilities
+ * (2^-11, or 2^-32 of the largest) and the dequantized keys and values.  A NaN in
+ * the params of a key or value reaches the queries that see its token, no
+ * others; a NaN or an infinity in a query reaches that token's head only.
+ * Queries and scores may have any size; lse is right for queries up to 2^90.
  *
  *   q          [in]  device, [T, heads_q, head_dim] of dtype (QG_F16 or
  *              QG_BF16); strides in elements, multiples of 8.  heads_q is a
@@ -607,7 +611,8 @@ qg_status qg_dequantize_kv4(const qg_kv4_cache *cache, const int64_t *slots, voi
  *   workspace  device scratch of qg_attention_kv4_workspace_size() bytes (0: may
  *              be NULL), 16-byte aligned, contents free before and after.  Calls
  *              that may run at the same time must not share it.
- * B is at most 4096.  A length or start outside its range is cut, a page index
+ * B is at most 4096 (0 only with T = 0 or q_starts), max_pages * page_size at
+ * most 2^31 - 128.  A length or start outside its range is cut, a page index
  * outside the cache is not read; the sequence's result is then undefined and
  * qg_check_device_errors returns QG_ERR_INVALID_ARG.
  */

@@ -33,14 +33,15 @@
 // 32 keys pass it by 8 binary digits: a vote instead of a reduction, and 32 keys
 // at a time keep a warp's state small.
 //
-// Measured, 64 sequences of 4096..8192 tokens, 64/8 heads of 128: 119 us, HBM's
+// Measured, 64 sequences of 4096..8192 tokens, 64/8 heads of 128: 122 us, HBM's
 // rate is 70.  A product takes the sub-core's issue for 8 cycles, in which no
 // other instruction goes out (probe: 8 products and 32 logic operations take 99
 // cycles, 64 and 64 alone), so 16 keys of 128 channels cost 16 products x 8 and
-// about 290 others, 170 of them on the half-rate ALU (masks, shifts, minima).
-// That is why the middle is an addition and not the other half of the products'
-// depth (24 products: 126 us).  About 12 us of a call are its beginning and end
-// (lengths, first loads, joins).
+// about 380 others (counted), 87 us of issue.  That is why the middle is an
+// addition and not the other half of the products' depth (24 products: 7 us
+// more).  About 12 us of a call are its beginning and end (lengths, first loads,
+// joins).  The rest, about 20, is latency: three warps a scheduler are ready to
+// issue 0.83 at a time, each a chain of load, product, vote, exponential, product.
 //
 // Every warp is a worker of its own: the chunks of tokens of all sequences
 // and heads form one list, split evenly over the warps of one CTA per SM, so
@@ -74,9 +75,9 @@ unsigned long long read_clear_status_attn(cudaStream_t s) {
 namespace {
 
 // The ring: 64 tokens a stage and 2 stages for each of 12 warps (221 KB at 128 channels, the registers' 168 a thread).
-// 64 sequences of 4096..8192 tokens, 64/8 heads of 128: 119 us (3.8 TB/s); 8 or 10 warps were 13 and 22 longer, stages
-// of 32 tokens 16.  Heads of 64 take 128 registers: 16 warps 81 us, 12 warps 6 more.  Two row tiles take 205 and more: 2 x
-// 131071 tokens, 4 new ones, 32/8 heads of 64: 73 us with 8 warps, not less with 12.
+// 64 sequences of 4096..8192 tokens, 64/8 heads of 128: 122 us (3.8 TB/s); 8 or 10 warps were 13 and 22 longer, stages
+// of 32 tokens 16.  Heads of 64 take 128 registers: 16 warps 71 us, 12 warps 6 more.  Two row tiles take 208 and more: 2 x
+// 131071 tokens, 4 new ones, 32/8 heads of 64: 76 us with 8 warps, not less with 12.
 constexpr int kChunk = 64;   // tokens per ring stage
 template <int G, int NT>
 constexpr int kWarpsOf = NT == 2 ? 8 : G == 1 ? 16 : 12;  // workers per CTA (registers: 65536 / (32 workers))
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<G, NT>, 1)
   pdl_trigger();
   // (Also behind the prompt kernel of the same call, with which it shares nothing but its inputs: only this wait makes
   // what earlier grids wrote visible.  Overlapped without it, 16 sequences of 4096 tokens, two with 512 new ones, took
-  // 111 instead of 121 us.)
+  // 112 instead of 122 us.)
   pdl_wait();
 
   // prefix[b]: chunks (times heads) of the sequences before b

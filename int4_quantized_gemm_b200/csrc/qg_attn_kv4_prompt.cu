@@ -29,11 +29,13 @@
 // of 0.00021: keys 0.00027, values 0.00020, p 0.00015.  Splitting keys into two
 // operands would take the first away for 1.4 times the tensor cores' time.)
 //
-// 2 x 4096 tokens, 32 heads of 128, causal: 340 us, 0.81 PFLOP/s.  A step of 64
-// keys by 256 rows takes 2250 cycles.  The tensor pipe is busy for 1590 of them
-// (a product of N 64 reads both operands from shared memory and takes 65 cycles
-// instead of 32); exponentials need 1024 of the MUFU.  The two tiles share both
-// units in phase, which leaves the rest.  Tried and slower: scores of 128 keys
+// 2 x 4096 tokens, 32 heads of 128, causal: 345 us in a row of 30 calls, 368 in
+// seconds of them, when the power limit lowers the clock (0.80 and 0.75 PFLOP/s).
+// A step of 64 keys by 256 rows takes about 2250 cycles.  The tensor cores hold
+// products for 1590 of them, of which 1020 are arithmetic (a product of N 64 reads
+// both operands from shared memory and takes 65 cycles instead of 32);
+// exponentials need 1024 of the MUFU.  The two tiles share both units in phase,
+// which leaves the rest.  Tried and slower: scores of 128 keys
 // at once (one place for S, 419 us), tiles taking turns at the tensor cores
 // (390), two threads a row, 16 warps of softmax (396), the maximum beside the
 // exponentials of a stale one (361), a part of the exponentials as polynomials.
@@ -44,8 +46,8 @@
 // output's columns back.
 //
 // With few (rows, head)s the keys are split over CTAs whose parts a second
-// kernel joins in order (16 sequences of 4096 tokens, two with 64 new tokens: 65
-// us, 98 without).
+// kernel joins in order (16 sequences of 4096 tokens, two with 64 new tokens: 75
+// us, 33 more without).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -881,8 +883,8 @@ int64_t row_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
 
 // Rows (query tokens x head group) that the decode kernel takes, in tiles of 8; 0: none.  A ragged call gives it
 // the sequences of 8 rows at most, or of 16 where one token has more than 8 or the mean sequence has 9 to 16 (drafts;
-// 64 sequences of 4096..8192 tokens, 32/8 heads of 128, 60 of them with 3 new tokens: 194 us, 488 with the prompt kernel for
-// these; but one of them with 3: 184, 149 with the prompt kernel for it).
+// 64 sequences of 4096..8192 tokens, 32/8 heads of 128, 60 of them with 3 new tokens: 180 us, 457 with the prompt kernel for
+// these; but one of them with 3: 170, 144 with the prompt kernel for it).
 int decode_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
   int64_t rows = T / B * group;
   if (ragged) rows = T * group > 8 * B && T * group <= 16 * B ? 16 : group;
@@ -890,7 +892,7 @@ int decode_tiles(int64_t B, int64_t T, int64_t group, bool ragged) {
 }
 
 // Blocks of a call, and those that leave parts (0: every tile's keys are one share, and the kernel without parts takes
-// them, 340 instead of 353 us for 2 x 4096 tokens of 32 heads).  The device counts a ragged call's tiles, but the query
+// them, 13 us less for 2 x 4096 tokens of 32 heads).  The device counts a ragged call's tiles, but the query
 // tokens that its sequences share make a least number of them, with which nothing is split.
 struct Blocks {
   int64_t all, parts;
