@@ -104,3 +104,20 @@ def test_zero_and_small_queries_with_a_small_scale(dtype, n, scale):
     qs[:, 1] *= 2.0 ** -10
     ref, _, bound, _ = exact(qs, kv, [n], scale)
     assert_close(call(qs, scale=scale), ref, bound)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 4, 40])
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 40, 2.0 ** 86])
+def test_the_log_sum_of_large_queries(D, n, size):
+    """Finite and right up to queries of 2^90."""
+    call, kv = setup(D)
+    qs = (queries(n, D, BF16).clamp(-7, 7).float() * size).to(BF16)
+    lse = torch.empty(n, 8, device="cuda")
+    out = call(qs, lse=lse)
+    assert torch.isfinite(out).all()
+    ref = exact(qs, kv, [n], D ** -0.5)[1]
+    k = kv[0][0].abs()
+    most = torch.stack([(qs[:, h].double().abs() @ k[h // 4].T).amax(1) for h in range(8)], 1) * D ** -0.5
+    # every product of the best key's score rounds by u at most, twice; binary32 sums and products
+    assert ((lse.double() - ref).abs() <= (2 * U + 2.0 ** -18) * most + 0.01).all()
